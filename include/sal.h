@@ -278,10 +278,11 @@ int sal_checked_build(void);
 
 /* Synchronises the current device and reports, then clears, the accesses the checked
  * build refused on it since the last report: their count, the lowest address, the source
- * file of that access (1 frontend.cu, 2 rowops.cu, 3 gemm.cu, 4 attention.cu, 5 ctc.cu)
- * and line, and the smallest sal_launch_count value before a launch that made one. All
- * outputs are 0 when count is 0. SAL_EINVAL (outputs 0) from libsal.so or on a null
- * pointer; SAL_ECUDA if the device cannot be reached. */
+ * file of that access (1 frontend.cu, 2 rowops.cu, 3 gemm.cu, 4 attention.cu, 5 ctc.cu,
+ * 6 window_attention.cu, 7 paged_attention.cu, 8 cache.cu) and line, and the smallest
+ * sal_launch_count value before a launch that made one. All outputs are 0 when count is 0.
+ * SAL_EINVAL (outputs 0) from libsal.so or on a null pointer; SAL_ECUDA if the device
+ * cannot be reached. */
 sal_status sal_check_report(uint64_t* count, uint64_t* first_address, int* file, int* line,
                             uint64_t* first_launch);
 
@@ -446,6 +447,140 @@ sal_status sal_attention_withhold(const void* q, const void* k, const void* v, i
 /* Row log-softmax (the adapter's last step): out[r, i] = z[r, i] - log sum_j exp z[r, j]
  * for i < n. z rows are ld floats apart (ld >= n), out rows n floats apart; float32. */
 sal_status sal_log_softmax(const float* z, int64_t rows, int n, int64_t ld, float* out, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Live streams: attention with a sliding window, a paged key/value cache, and the
+ * attention of one new position over it. The page's local encoder windows ("Nemotron 3.5
+ * Transcribe: From Recorded Speech to Dataset Audits", section "Local encoder windows,
+ * recording-wide language context") bound what a position sees by cutting the recording;
+ * these calls bound it by a window that moves with the position, so that a recording can
+ * be encoded while it is still being made. The page describes no such mode: the mask and
+ * the cache are this library's own.
+ *
+ * One mask for all of them: in a sequence of n positions, key j is visible to position p
+ * when
+ *     0 <= j < n   and   j <= p + right   and   (j >= p - left or j < sinks).
+ * `sinks` first positions stay visible however far the window has moved. A negative left
+ * or right is no limit. Keys and values at visible positions and at other positions of
+ * [0, n) must be finite; what memory holds past n is never used.
+ * --------------------------------------------------------------------------------- */
+
+typedef struct {
+  int64_t left;  /* positions before p that are visible (< 0: all) */
+  int64_t right; /* positions after p that are visible (< 0: all; 0: causal) */
+  int64_t sinks; /* first positions that are always visible up to p + right (>= 0) */
+} sal_window;
+
+/* Windowed attention, the masked form of sal_attention_heads: q [batch, heads, T,
+ * head_dim], k and v [batch, kv_heads, T, head_dim] bf16; o [batch, T, heads * head_dim]
+ * bf16 = softmax(q k^T / sqrt(head_dim)) v over the visible keys. Query head h reads
+ * key/value head h / (heads / kv_heads). lengths: int32 [batch], positions of each clip
+ * (clamped to [0, T]; may be NULL: all T); rows of o at or past a clip's length are left
+ * as they were. window may be NULL (no limit on either side). o must not overlap the
+ * inputs. Errors: SAL_EINVAL (negative count, null or misaligned pointer, negative sinks,
+ * kv_heads that does not divide heads), SAL_ESHAPE (head_dim not 64 or 128, T > 90,000,
+ * batch * heads > 65,535), SAL_EDEVICE, SAL_ECUDA. */
+sal_status sal_attention_window(const void* q, const void* k, const void* v, int batch, int64_t T, int heads,
+                                int kv_heads, int head_dim, const sal_window* window, const int32_t* lengths,
+                                void* o, void* stream);
+
+#define SAL_CACHE_MAX_PAGES 524288
+#define SAL_CACHE_MAX_SEQUENCES 32768
+
+/* Bits of a cache's status word (device memory; the calls set bits and never clear them). */
+#define SAL_CACHE_NO_PAGES 1u /* a sequence could not grow: too few free pages */
+#define SAL_CACHE_BAD_LIST 2u /* an index or length out of range, or a sequence named twice */
+
+/* A paged key/value cache: a record of the caller's device buffers (the record itself is
+ * host memory, read during a call only). Position p of sequence s is row p % page_size of
+ * page table[s][p / page_size]; sequence s holds positions [0, lengths[s]). The tables are
+ * the whole state: a page is in use when one of the first ceil(lengths[s] / page_size)
+ * entries of some row s names it, and free otherwise. Rows may share pages. A used entry
+ * outside [0, pages) (-1 by convention) is a page that has been let go: its positions are
+ * invisible. Calls on one cache must be ordered (one stream, or events between streams).
+ *   k, v        [layers, pages, kv_heads, page_size, head_dim] bf16, 16-byte aligned
+ *   table       [sequences, max_pages] int32     lengths  [sequences] int32
+ *   status      one uint32 that failed operations set bits of
+ *   workspace   sal_cache_workspace_bytes() bytes, 256-byte aligned; used by resize and
+ *               compact (may be NULL for the other calls)
+ * page_size is a power of two in [8, 256], head_dim 64 or 128, pages at most
+ * SAL_CACHE_MAX_PAGES, sequences at most SAL_CACHE_MAX_SEQUENCES, layers at most 32,767,
+ * kv_heads at most 65,535, max_pages * page_size at most 2^28. Every call returns SAL_EINVAL for a null, misaligned (16 bytes; table,
+ * lengths, status: 4) or negative member and SAL_ESHAPE for one out of these ranges. */
+typedef struct {
+  void *k, *v;
+  int layers, pages, kv_heads, page_size, head_dim;
+  int sequences, max_pages;
+  int32_t *table, *lengths;
+  uint32_t* status;
+  void* workspace;
+  size_t workspace_bytes;
+} sal_cache;
+
+/* Bytes of sal_cache.workspace for a cache of these sizes (0 when either is <= 0). */
+size_t sal_cache_workspace_bytes(int pages, int sequences);
+
+/* Writes new keys and values into a layer's pages: token t of row b, k and v [batch,
+ * kv_heads, T, head_dim] bf16, goes to position starts[b] + t of sequence seqs[b] (NULL:
+ * b). Tokens at positions outside [0, lengths[seq]), or whose page has been let go, and
+ * rows with a sequence out of range, are skipped: so a row may bring fewer than T tokens,
+ * and one whose sal_cache_resize failed writes nothing. Two tokens for one position (a
+ * sequence named twice, or a page that two rows share) leave one of them there. */
+sal_status sal_cache_append(const sal_cache* cache, int layer, const void* k, const void* v, int batch, int64_t T,
+                            const int32_t* starts, const int32_t* seqs, void* stream);
+
+/* Copies whole pages in every layer: page src[i] to page dst[i] for i < n. Pairs with a
+ * page out of range are skipped and set SAL_CACHE_BAD_LIST. A page that is a destination
+ * of two pairs, or the source of one and the destination of another, ends up with
+ * unspecified contents. The tables are not touched. */
+sal_status sal_cache_copy_pages(const sal_cache* cache, const int32_t* src, const int32_t* dst, int n, void* stream);
+
+/* The three calls below compute new tables from cache->table and cache->lengths and write
+ * them to table_out and lengths_out: the same arrays (the cache changes in place), or
+ * arrays of the same shape that overlap nothing else, which receive every row, listed or
+ * not, while the old ones stay valid for work still queued on them. Lists are int32 device
+ * arrays of n <= sequences entries. An index out of [0, sequences), a sequence that is
+ * changed twice, or a length out of [0, max_pages * page_size] sets SAL_CACHE_BAD_LIST in
+ * *status, and then the whole call changes nothing (the outputs are copies). */
+
+/* Sequence dst[i] becomes a fork of src[i]: it gets its length and shares its pages (what
+ * dst[i] held is dropped). All sources are read before any is replaced, so a list may
+ * permute or multiply sequences (src may repeat, dst may not). No page is copied: a shared
+ * page that a later sal_cache_resize is about to let grow is copied by it. */
+sal_status sal_cache_fork(const sal_cache* cache, const int32_t* src, const int32_t* dst, int n, int32_t* table_out,
+                          int32_t* lengths_out, void* stream);
+
+/* Gives sequence seqs[i] the length new_lengths[i]: shorter drops positions from the end (0
+ * frees the sequence), longer makes room for positions that sal_cache_append then writes.
+ * window (may be NULL: keep everything; its `right` is not used) lets go of the pages that
+ * no position from min(old, new length) on can see. First all listed sequences are cut and
+ * their unseen pages let go; then, in the order of the list, each that grows gets a page
+ * for every new table entry, and a replacement for a partly filled last page that is
+ * shared with another row (its contents copied in every layer) or that was let go. The
+ * pages handed out are the free ones in ascending order. Entries past a listed sequence's
+ * last page become -1. Too few free pages set SAL_CACHE_NO_PAGES, and the call changes
+ * nothing. */
+sal_status sal_cache_resize(const sal_cache* cache, const int32_t* seqs, const int32_t* new_lengths, int n,
+                            const sal_window* window, int32_t* table_out, int32_t* lengths_out, void* stream);
+
+/* Moves the m pages in use to the numbers [0, m): the i-th used page numbered m or higher
+ * (ascending) moves to the i-th free page below m, in every layer, and table_out names the
+ * new places (entries that are not used become -1). The pages moved from keep their
+ * contents until they are handed out again. */
+sal_status sal_cache_compact(const sal_cache* cache, int32_t* table_out, int32_t* lengths_out, void* stream);
+
+/* Attention of one position per row, the newest of its sequence, over a layer of the
+ * cache: row b is position p = lengths[seq] - 1 of sequence seqs[b] (NULL: b). q: head h of
+ * row b at q + b * q_row_stride + h * q_head_stride (elements; multiples of 8), bf16; o
+ * [batch, heads * head_dim] bf16. window may be NULL; its `right` is not used. A row with
+ * nothing visible (length 0, a sequence out of range, every page let go) gives zeros.
+ * workspace: sal_attention_paged_workspace_bytes() bytes, 256-byte aligned; calls that may
+ * overlap on the GPU need workspaces of their own. Errors: SAL_EINVAL, SAL_ESHAPE (batch
+ * or heads > 65,535), SAL_EWORKSPACE, SAL_EDEVICE, SAL_ECUDA. */
+size_t sal_attention_paged_workspace_bytes(const sal_cache* cache, int batch, int heads);
+sal_status sal_attention_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride, int batch, int heads,
+                               const sal_cache* cache, int layer, const int32_t* seqs, const sal_window* window,
+                               void* o, void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }

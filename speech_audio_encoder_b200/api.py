@@ -65,6 +65,21 @@ class sal_forward_options(ctypes.Structure):
 WINDOW_CORE, WINDOW_CONTEXT = 500, 50  # the serving-window defaults (sal.h)
 
 
+class sal_window(ctypes.Structure):
+    _fields_ = [("left", ctypes.c_int64), ("right", ctypes.c_int64), ("sinks", ctypes.c_int64)]
+
+
+class sal_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("layers", ctypes.c_int), ("pages", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("page_size", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("sequences", ctypes.c_int), ("max_pages", ctypes.c_int), ("table", ctypes.c_void_p),
+                ("lengths", ctypes.c_void_p), ("status", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+CACHE_NO_PAGES, CACHE_BAD_LIST = 1, 2  # bits of a cache's status word (sal.h)
+
+
 KIND_NAMES = ["rope_table", "layernorm", "qkv", "attention", "out_proj", "ffn_up", "ffn_down"]
 
 EXPORTS = {
@@ -135,6 +150,29 @@ EXPORTS = {
     "sal_ctc_adapter": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64,
                                         ctypes.POINTER(sal_ctc_weights), ctypes.c_void_p, ctypes.c_void_p,
                                         ctypes.c_size_t, ctypes.c_void_p]),
+    "sal_attention_window": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                             ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                             ctypes.POINTER(sal_window), ctypes.c_void_p, ctypes.c_void_p,
+                                             ctypes.c_void_p]),
+    "sal_cache_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int]),
+    "sal_cache_append": (ctypes.c_int, [ctypes.POINTER(sal_cache), ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.c_void_p]),
+    "sal_cache_copy_pages": (ctypes.c_int, [ctypes.POINTER(sal_cache), ctypes.c_void_p, ctypes.c_void_p,
+                                             ctypes.c_int, ctypes.c_void_p]),
+    "sal_cache_fork": (ctypes.c_int, [ctypes.POINTER(sal_cache), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "sal_cache_resize": (ctypes.c_int, [ctypes.POINTER(sal_cache), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                         ctypes.POINTER(sal_window), ctypes.c_void_p, ctypes.c_void_p,
+                                         ctypes.c_void_p]),
+    "sal_cache_compact": (ctypes.c_int, [ctypes.POINTER(sal_cache), ctypes.c_void_p, ctypes.c_void_p,
+                                          ctypes.c_void_p]),
+    "sal_attention_paged_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(sal_cache), ctypes.c_int,
+                                                               ctypes.c_int]),
+    "sal_attention_paged": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
+                                            ctypes.c_int, ctypes.POINTER(sal_cache), ctypes.c_int, ctypes.c_void_p,
+                                            ctypes.POINTER(sal_window), ctypes.c_void_p, ctypes.c_void_p,
+                                            ctypes.c_size_t, ctypes.c_void_p]),
 }
 
 _libs: dict = {}
@@ -504,7 +542,8 @@ def sal_set_wait_limit_ns(ns: int) -> None:
     lib().sal_set_wait_limit_ns(int(ns))
 
 
-FILE_IDS = {1: "frontend.cu", 2: "rowops.cu", 3: "gemm.cu", 4: "attention.cu", 5: "ctc.cu"}
+FILE_IDS = {1: "frontend.cu", 2: "rowops.cu", 3: "gemm.cu", 4: "attention.cu", 5: "ctc.cu",
+            6: "window_attention.cu", 7: "paged_attention.cu", 8: "cache.cu"}
 
 
 def check_report() -> dict:
@@ -568,3 +607,178 @@ def attention_plan(batch: int, T: int, heads: int = 10, head_dim: int = 128, sms
     _check("sal_attention_plan", lib().sal_attention_plan(batch, T, heads, head_dim, sms, ctypes.byref(p),
                                                           ctypes.byref(q)))
     return p.value, q.value
+
+
+# ----------------------------------------------------------------------------- live streams
+
+def _operand(name: str, t: torch.Tensor, dtype, shape=None) -> int:
+    """The address of a contiguous tensor of this type (and shape) on the current device."""
+    if t.dtype is not dtype or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name}: expected {dtype}{'' if shape is None else ' of shape ' + str(tuple(shape))}, got "
+                         f"{t.dtype} of shape {tuple(t.shape)}")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: must be on the current CUDA device")
+    return _ptr(t)
+
+
+def _list_operand(name: str, t: torch.Tensor | None, n: int | None = None) -> int:
+    """The address of a one-dimensional int32 device tensor (of n entries), 0 for None."""
+    if t is None:
+        return 0
+    if t.dim() != 1:
+        raise ValueError(f"{name}: expected one dimension, got {t.dim()}")
+    return _operand(name, t, torch.int32, None if n is None else (n,))
+
+
+def sal_attention_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, left: int = -1, right: int = -1,
+                         sinks: int = 0, lengths: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """q [batch, heads, T, head_dim], k and v [batch, kv_heads, T, head_dim] bf16 -> o [batch * T, heads * head_dim]:
+    position p sees the keys j <= p + right with j >= p - left or j < sinks (a negative left or right is no limit).
+    ``lengths`` [batch] int32: positions of each clip; rows of ``out`` past them are left as they were (a tensor made
+    here starts as zeros then)."""
+    B, H, T, hd = q.shape
+    kvh = k.shape[1] if k.dim() == 4 else 0
+    if out is None:
+        out = (torch.empty if lengths is None else torch.zeros)((B * T, H * hd), dtype=torch.bfloat16, device=q.device)
+    kv = (B, kvh, T, hd)
+    win = sal_window(left, right, sinks)
+    _check("sal_attention_window", lib().sal_attention_window(
+        _operand("q", q, torch.bfloat16), _operand("k", k, torch.bfloat16, kv), _operand("v", v, torch.bfloat16, kv), B,
+        T, H, kvh, hd, ctypes.byref(win), _list_operand("lengths", lengths, B),
+        _operand("out", out, torch.bfloat16, (B * T, H * hd)), _stream(stream)))
+    return out
+
+
+class PagedCache:
+    """Keys and values of live sequences in pages (sal_cache in sal.h), in the caller's tensors:
+
+    k, v [layers, pages, kv_heads, page_size, head_dim] bf16, table [sequences, max_pages] int32 and lengths
+    [sequences] int32 (the tables are the whole state: a page that no row uses is free). ``empty`` makes a cache
+    without sequences; ``with_tables`` makes another view of the same pages, for calls that leave the old tables valid.
+    Failed operations set bits of ``status`` (CACHE_NO_PAGES, CACHE_BAD_LIST); ``check`` reads it.
+    """
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor,
+                 status: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+        layers, pages, kv_heads, page_size, head_dim = k.shape
+        sequences, max_pages = table.shape
+        if status is None:
+            status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        if workspace is None:
+            n = lib().sal_cache_workspace_bytes(pages, sequences)
+            workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=k.device)
+        self.k, self.v, self.table, self.lengths = k, v, table, lengths
+        self.status, self.workspace = status, workspace
+        self.record = sal_cache(
+            _operand("k", k, torch.bfloat16), _operand("v", v, torch.bfloat16, k.shape), layers, pages, kv_heads,
+            page_size, head_dim, sequences, max_pages, _operand("table", table, torch.int32),
+            _operand("lengths", lengths, torch.int32, (sequences,)), _operand("status", status, torch.int32, (1,)),
+            _operand("workspace", workspace, torch.uint8), workspace.numel())
+        self.ref = ctypes.byref(self.record)
+
+    @classmethod
+    def empty(cls, layers: int, pages: int, kv_heads: int, page_size: int, head_dim: int, sequences: int,
+              max_pages: int, device="cuda") -> "PagedCache":
+        shape = (layers, pages, kv_heads, page_size, head_dim)
+        return cls(torch.empty(shape, dtype=torch.bfloat16, device=device),
+                   torch.empty(shape, dtype=torch.bfloat16, device=device),
+                   torch.full((sequences, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros(sequences, dtype=torch.int32, device=device))
+
+    def with_tables(self, table: torch.Tensor, lengths: torch.Tensor) -> "PagedCache":
+        """The same pages under other tables of the same shape."""
+        if table.shape != self.table.shape:
+            raise ValueError("with_tables: the tables must have the cache's shape")
+        return PagedCache(self.k, self.v, table, lengths, self.status, self.workspace)
+
+    def check(self) -> None:
+        """Waits for the device and raises if an operation has failed since the last check."""
+        bits = int(self.status.item())
+        if bits:
+            self.status.zero_()
+            what = [w for b, w in ((CACHE_NO_PAGES, "too few free pages"),
+                                   (CACHE_BAD_LIST, "a list with an index or length out of range, or a sequence twice"))
+                    if bits & b]
+            raise RuntimeError("cache operation failed: " + "; ".join(what))
+
+    def _tables_of(self, out: "PagedCache | None") -> tuple:
+        out = self if out is None else out
+        if out.table.shape != self.table.shape or out.k.data_ptr() != self.k.data_ptr():
+            raise ValueError("out: must be this cache's pages under tables of the same shape")
+        return out, out.record.table, out.record.lengths
+
+
+def sal_cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor,
+                     seqs: torch.Tensor | None = None, layer: int = 0, stream=None) -> None:
+    """k, v [batch, kv_heads, T, head_dim] bf16 into positions starts[b] + t of sequences seqs[b] (None: b)."""
+    B, kvh, T, hd = k.shape
+    if (kvh, hd) != (cache.record.kv_heads, cache.record.head_dim):
+        raise ValueError(f"k: the cache has {cache.record.kv_heads} heads of {cache.record.head_dim}")
+    _check("sal_cache_append", lib().sal_cache_append(
+        cache.ref, layer, _operand("k", k, torch.bfloat16), _operand("v", v, torch.bfloat16, k.shape), B, T,
+        _list_operand("starts", starts, B), _list_operand("seqs", seqs, B), _stream(stream)))
+
+
+def sal_cache_copy_pages(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
+    """Page src[i] to page dst[i] in every layer (the tables are not touched)."""
+    n = src.shape[0]
+    _check("sal_cache_copy_pages", lib().sal_cache_copy_pages(
+        cache.ref, _list_operand("src", src), _list_operand("dst", dst, n), n, _stream(stream)))
+
+
+def sal_cache_fork(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor, out: PagedCache | None = None,
+                   stream=None) -> PagedCache:
+    """Sequences dst[i] become forks of src[i]; the new tables go to ``out`` (None: in place)."""
+    out, table, lengths = cache._tables_of(out)
+    n = src.shape[0]
+    _check("sal_cache_fork", lib().sal_cache_fork(
+        cache.ref, _list_operand("src", src), _list_operand("dst", dst, n), n, table, lengths, _stream(stream)))
+    return out
+
+
+def sal_cache_resize(cache: PagedCache, seqs: torch.Tensor, new_lengths: torch.Tensor, left: int = -1, sinks: int = 0,
+                     out: PagedCache | None = None, stream=None) -> PagedCache:
+    """Sequences seqs[i] get the length new_lengths[i] (0 frees them); with left >= 0 the pages that no later
+    position sees are let go. The new tables go to ``out`` (None: in place)."""
+    out, table, lengths = cache._tables_of(out)
+    n = seqs.shape[0]
+    win = sal_window(left, 0, sinks)
+    _check("sal_cache_resize", lib().sal_cache_resize(
+        cache.ref, _list_operand("seqs", seqs), _list_operand("new_lengths", new_lengths, n), n, ctypes.byref(win),
+        table, lengths, _stream(stream)))
+    return out
+
+
+def sal_cache_compact(cache: PagedCache, out: PagedCache | None = None, stream=None) -> PagedCache:
+    """Moves the pages in use to the lowest numbers; the new tables go to ``out`` (None: in place)."""
+    out, table, lengths = cache._tables_of(out)
+    _check("sal_cache_compact", lib().sal_cache_compact(cache.ref, table, lengths, _stream(stream)))
+    return out
+
+
+def attention_paged_workspace(cache: PagedCache, batch: int, heads: int) -> torch.Tensor:
+    n = lib().sal_attention_paged_workspace_bytes(cache.ref, batch, heads)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=cache.k.device)
+
+
+def sal_attention_paged(q: torch.Tensor, cache: PagedCache, left: int = -1, sinks: int = 0, layer: int = 0,
+                        seqs: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """q [batch, heads, head_dim] bf16 (any strides of its first two dimensions that are multiples of 8), the newest
+    position of sequences seqs[b] (None: b) -> o [batch, heads * head_dim]."""
+    B, H, hd = q.shape
+    if hd != cache.record.head_dim or q.stride(2) != 1:
+        raise ValueError(f"q: expected contiguous heads of {cache.record.head_dim}")
+    if q.dtype is not torch.bfloat16 or not q.is_cuda or q.device.index != torch.cuda.current_device():
+        raise ValueError("q: expected bfloat16 on the current CUDA device")
+    if out is None:
+        out = torch.empty((B, H * hd), dtype=torch.bfloat16, device=q.device)
+    if workspace is None:
+        workspace = attention_paged_workspace(cache, B, H)
+    win = sal_window(left, 0, sinks)
+    _check("sal_attention_paged", lib().sal_attention_paged(
+        q.data_ptr(), q.stride(0), q.stride(1), B, H, cache.ref, layer, _list_operand("seqs", seqs, B),
+        ctypes.byref(win), _operand("out", out, torch.bfloat16, (B, H * hd)),
+        _operand("workspace", workspace, torch.uint8), workspace.numel(), _stream(stream)))
+    return out

@@ -149,6 +149,8 @@ bool is_device_ptr(const void* p) {
 
 }  // namespace
 
+sal_status require_device() { return check_device(); }
+
 uint64_t wait_limit_ns() { return g_wait_limit_ns.load(); }
 
 Windows make_windows(int64_t total, int64_t core, int64_t ctx) {

@@ -48,6 +48,7 @@ struct NvtxRange {
   NvtxRange& operator=(const NvtxRange&) = delete;
 };
 
+sal_status require_device();  // SAL_OK when the current device is an sm_100 GPU
 uint64_t wait_limit_ns();
 bool pdl_enabled();  // programmatic dependent launch (env SAL_PDL=0 turns it off)
 void count_launch();  // one kernel enqueued
@@ -105,6 +106,14 @@ sal_status attention_launch_heads(const void* q, const void* k, const void* v, i
 sal_status ctc_qk_norm_rope_launch(const float* qkv, int64_t rows, int64_t T, const void* qn_g, const void* kn_g,
                                    const float* cs, void* q, void* k, void* v, cudaStream_t s);
 sal_status log_softmax_launch(const float* z, int64_t rows, int n, int64_t ld, float* out, cudaStream_t s);
+
+// window_attention.cu
+sal_status window_attention_launch(const void* q, const void* k, const void* v, int batch, int64_t T, int heads,
+                                   int kv_heads, int head_dim, const sal_window& win, const int32_t* lengths, void* o,
+                                   cudaStream_t s);
+
+// cache.cu
+sal_status check_cache(const sal_cache* c, bool workspace);  // the members of a cache record
 
 // tensor maps (sal_api.cu)
 bool make_tmap_2d_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
