@@ -230,8 +230,8 @@ def _ptr(t) -> int:
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the current stream's handle, without making a Stream object for it
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -616,9 +616,11 @@ def _operand(name: str, t: torch.Tensor, dtype, shape=None) -> int:
     if t.dtype is not dtype or (shape is not None and t.shape != shape):
         raise ValueError(f"{name}: expected {dtype}{'' if shape is None else ' of shape ' + str(tuple(shape))}, got "
                          f"{t.dtype} of shape {tuple(t.shape)}")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{name}: must be on the current CUDA device")
-    return _ptr(t)
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libsal must be contiguous")
+    return t.data_ptr()
 
 
 def _list_operand(name: str, t: torch.Tensor | None, n: int | None = None) -> int:
