@@ -55,4 +55,79 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t saddr, uint32_t rank) {
   return v;
 }
 
+// mbar_wait of sal_ptx.cuh for kernels whose code has to stay small: asleep in the hardware for
+// up to 20 us at a time instead of polling, so that waiting warps leave the issue slots of their SM
+// sub-partition to the warps that compute. A wait that gives up (its limit, or another role's
+// abort flag) only returns false; the role ends and calls give_up once. The _warp form is for a
+// whole warp, whose lanes all get the same answer.
+__device__ __forceinline__ bool mbar_sleep_once(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 20000;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity, const WaitGuard& g) {
+  if (mbar_sleep_once(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  do {
+    if (mbar_sleep_once(bar, parity)) return true;
+  } while (*g.abort == 0 && globaltimer_ns() - t0 <= g.limit_ns);
+  return false;
+}
+__device__ __forceinline__ bool mbar_sleep_warp(uint64_t* bar, uint32_t parity, const WaitGuard& g) {
+  return __all_sync(0xffffffffu, mbar_sleep(bar, parity, g));
+}
+__device__ __forceinline__ void give_up(const WaitGuard& g) {
+  if (*g.abort) return;
+  *g.abort = 1;
+  atomicOr(g.status, kStatusTimeout);
+}
+
+// Matrix products for a warp whose lanes all reach them: `one` is non-zero in the one lane that
+// issues. With the choice of the lane inside the instruction the code around it stays
+// warp-uniform, so descriptors are computed and passed in uniform registers; behind a branch on
+// the lane every operand is moved there one by one for every product.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, e;\n\t}\n"
+      : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void umma_ss_one(uint32_t one, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void umma_ts_one(uint32_t one, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_one(uint32_t one, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_u32(bar)),
+      "r"(one)
+      : "memory");
+}
+
 }  // namespace sal

@@ -8,20 +8,23 @@
 // limit cuts. A block holds two query tiles ("slots") that share every key tile it loads: two
 // query heads of one key head where heads come in such pairs (both see the same tiles), else two
 // neighbouring tiles of one head (a tile that only one of them sees is skipped by the other).
-// The tensor core reads 64 KB of K and V for 4 * 128 * 128 * 128 flops of one slot; without
-// the second slot the loads from L2 would bound it.
+// One slot alone would read 64 KB of K and V from L2 for every 4 * 128 * 128 * 128 flops, more than
+// L2 gives all SMs at the tensor core's rate.
 //
 // Windows are short (a minute is six tiles), so starting and ending would cost as much as the
-// work: the blocks are persistent, one per SM, and every role runs ahead into the next work item
-// as far as its buffers allow - the next Q and K are loaded while the last products run, and
-// one slot stores its rows while the other still multiplies.
+// work: the blocks are persistent, one per SM, and the slots run independently of each other.
+// Each has its own issuing warp, score columns, softmax warps and barriers, and takes the key
+// tiles from the common ring at its own pace, so that one slot ends an item and stores its rows
+// while the other multiplies.
 //
-// Roles: warp 0 loads (TMA); warp 1 issues S_i = Q_i K^T; warp 2 issues O_i += P_i V; warps 4-7 and
-// 8-11 are the softmax of slot 0 and 1, one row per thread. TMEM: at head dim 128 one score
-// buffer S [0,128) that the slots take in turn (a slot copies its scores to registers and hands
-// it back), O0 [128,256) O1 [256,384) P0 [384,448) P1 [448,512); at 64 a buffer each: S0 [0,128)
-// S1 [128,256) O0 [256,320) O1 [320,384), P as above. P is rounded to bf16 for its product
-// (the row sum is not); scores, maxima, sums and O are fp32.
+// Roles: warp 0 loads keys and values (TMA); warps 1 and 2 issue the products of slot 0 and 1;
+// warp 3 works out the items and loads their queries; warps 4-7 and 8-11 are the softmax of slot 0
+// and 1, one row per thread. TMEM, 256 columns per slot: at head dim 128 S (128) and O (128), the
+// weights P over the scores they were made from; S of the next tile then follows P V in the
+// tensor core's queue, and the other slot works meanwhile. At 64 there is room for S (128), P (64) and
+// O (64), and the next S goes ahead of P V. P V starts on the first 64 keys while the weights of the
+// others are computed. P is rounded to bf16 for its product (the row sum is not); scores, maxima,
+// sums and O are fp32.
 #define SAL_CK_FILE 6
 #include <cuda_bf16.h>
 #include <math.h>
@@ -30,32 +33,36 @@
 #include <mutex>
 
 #include "sal_internal.h"
-#include "sal_ptx.cuh"
+#include "sal_mma.cuh"
 
 namespace sal {
 namespace {
 
-constexpr int kTile = 128;
-constexpr int kBox = kTile * 64 * 2;       // one 64-column half of a 128 x 128 bf16 tile
+constexpr int kTile = 128;  // query rows of a slot
+constexpr int kKeys = 128;  // keys of a tile
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: below it the old maximum stays (p <= 256)
 constexpr int kThreads = 384;
-constexpr int kRegsCtrl = 104, kRegsSoftmax = 200;
-constexpr int kRegsNeeded = kRegsCtrl * 128 + kRegsSoftmax * 256;  // <= launch registers x 384
-constexpr int kLengths = 512;  // clip lengths kept in shared memory
+constexpr int kRegsLaunch = 168, kRegsCtrl = 104, kRegsSoftmax = 200;
+static_assert(kRegsCtrl * 128 + kRegsSoftmax * 256 <= kRegsLaunch * kThreads, "the split fits the launch's registers");
 
 template <int HD>
 struct Layout {
-  static constexpr int kTileB = kTile * HD * 2;  // a 128-row tile of Q, K or V
+  static constexpr int kQB = kTile * HD * 2;     // a slot's Q
+  static constexpr int kKB = kKeys * HD * 2;     // a tile of K or V
   static constexpr int kBoxes = HD / 64;         // 64-column boxes of a tile
-  static constexpr bool kSharedS = HD == 128;
-  static constexpr int kStages = 2;
-  static constexpr size_t kSmem = 1024 + (2 + 2 * kStages) * static_cast<size_t>(kTileB) + 512 + 4 * kLengths;
+  static constexpr int kBox = 128 * 64 * 2;
+  static constexpr int kStagesK = HD == 128 ? 3 : 4, kStagesV = HD == 128 ? 2 : 4;
+  static constexpr int kCtrlB = 1024;            // barriers and the work items
+  static constexpr size_t kSmem =
+      1024 + 2 * static_cast<size_t>(kQB) + (kStagesK + kStagesV) * static_cast<size_t>(kKB) + kCtrlB;
+  static constexpr bool kSharedS = HD == 128;    // one score buffer for both slots
   __device__ static uint32_t col_s(int i) { return kSharedS ? 0u : 128u * i; }
   __device__ static uint32_t col_o(int i) { return kSharedS ? 128u + 128u * i : 256u + 64u * i; }
   __device__ static uint32_t col_p(int i) { return 384u + 64u * i; }
 };
 static_assert(Layout<128>::kSmem <= 227 * 1024 && Layout<64>::kSmem <= 227 * 1024, "shared memory");
 
+constexpr int kItems = 4;  // work items published ahead
 enum Pairing { kSingles, kTilePairs, kHeadPairs };
 
 struct WindowArgs {
@@ -65,27 +72,36 @@ struct WindowArgs {
   int left, right, sinks;  // left, right: T for no limit
   int tiles;               // query tiles of a clip
   int pairing, items;
+  int wide;                // o is 32-byte aligned
   float scale_log2;
   uint64_t limit_ns;
   unsigned int* status;
 };
 
-// One work item: up to two query tiles and the key tiles they share. Key tile x of the item is
-// tile(x) of the clip: x < first are those of the first positions, then the window's.
+// One work item: up to two query tiles and the key tiles they share. Its first tiles hold the
+// first positions; the window's tiles start at the first key that any row of the item sees,
+// wherever that is (the copies may start at any row), so the fewest tiles cover it. Where the
+// first positions reach up to the window the tiles run on from position 0.
 struct Item {
-  int b, n, kv;               // clip, its length, its (clip, key head) plane
-  int head[2], row[2];        // query head and first row of each slot
-  int lo[2], hi[2], sink[2];  // a slot's window tiles [lo, hi) and first-position tiles [0, sink); hi = 0: empty
-  int first, w0, count;
-  __device__ int tile(int x) const { return x < first ? x : w0 + (x - first); }
-  __device__ bool uses(int i, int x) const {
-    const int t = tile(x);
-    return t < hi[i] && (t >= lo[i] || t < sink[i]);
+  int b, n, kv;         // clip, its length, its (clip, key head) plane
+  int head[2], row[2];  // query head and first row of each slot
+  int lo[2], hi[2];     // keys [lo, hi) that a slot's window reaches (hi = 0: an empty slot)
+  int first, start;     // tiles of first positions, first key of the window's tiles
+  int begin[2], last[2];  // the window's tiles [begin, last] that a slot uses, behind those of the first positions
+  int count, sinks;     // all tiles; the first positions
+  int nth[2];           // items that a slot took part in before this one
+
+  __device__ int base(int x) const { return x < first ? kKeys * x : start + kKeys * (x - first); }
+  __device__ bool uses(int i, int x) const { return x <= last[i] && (x < first || x >= begin[i]); }
+  __device__ int first_used(int i) const { return first > 0 ? 0 : begin[i]; }
+  __device__ int next_used(int i, int x) const { return x + 1 == first ? begin[i] : x + 1; }
+  // keys of tile x that the slot multiplies with: a multiple of 16, the rest of the tile is not used
+  __device__ int cols(int i, int x) const {
+    return min(kKeys, ((x < first ? sinks : hi[i]) - base(x) + 15) & ~15);
   }
-  __device__ int last(int i) const { return first + hi[i] - 1 - w0; }  // the slot's last x
 };
 
-__device__ __forceinline__ Item item_of(const WindowArgs& a, int idx, const int* lens) {
+__device__ __forceinline__ Item item_of(const WindowArgs& a, int idx) {
   Item it;
   // the rows of the longest reach (a causal clip's last tiles) come first
   int h, t0;
@@ -101,40 +117,55 @@ __device__ __forceinline__ Item item_of(const WindowArgs& a, int idx, const int*
     t0 = a.pairing == kTilePairs ? 2 * ((a.tiles + 1) / 2 - 1 - idx / planes) : a.tiles - 1 - idx / planes;
   }
   it.n = a.T;
-  if (a.lengths) it.n = min(max(it.b < kLengths ? lens[it.b] : *SAL_CK_LD(a.lengths + it.b, 4), 0), a.T);
+  if (a.lengths) it.n = min(max(*SAL_CK_LD(a.lengths + it.b, 4), 0), a.T);
   it.kv = it.b * a.kv_heads + h / (a.heads / a.kv_heads);
-  it.w0 = 1 << 30;
-  int w1 = 0, sinks = 0;
+  it.start = 1 << 30;
+  int end = 0;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     it.head[i] = h + (a.pairing == kHeadPairs ? i : 0);
     it.row[i] = kTile * (t0 + (a.pairing == kTilePairs ? i : 0));
-    it.lo[i] = it.hi[i] = it.sink[i] = 0;
+    it.lo[i] = it.hi[i] = 0;
     if (it.row[i] >= it.n || (i == 1 && a.pairing == kSingles)) continue;
-    const int end = min(it.n, min(it.row[i] + kTile, it.n) + a.right);  // keys below it are in reach
-    it.lo[i] = max(0, it.row[i] - a.left) / kTile;
-    it.hi[i] = (end + kTile - 1) / kTile;
-    it.sink[i] = (min(a.sinks, end) + kTile - 1) / kTile;
-    it.w0 = min(it.w0, it.lo[i]);
-    w1 = max(w1, it.hi[i]);
-    sinks = max(sinks, it.sink[i]);
+    it.lo[i] = max(0, it.row[i] - a.left);
+    it.hi[i] = min(it.n, min(it.row[i] + kTile, it.n) + a.right);
+    it.start = min(it.start, it.lo[i]);
+    end = max(end, it.hi[i]);
   }
-  it.first = min(it.w0, sinks);
-  it.count = w1 > 0 ? it.first + w1 - it.w0 : 0;
+  it.sinks = a.sinks;
+  it.first = 0;
+  if (a.sinks >= it.start)
+    it.start = 0;
+  else
+    it.first = (a.sinks + kKeys - 1) / kKeys;
+  it.count = end > 0 ? it.first + (end - it.start + kKeys - 1) / kKeys : 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    // (tiles that only the first positions reach into exist only where they run on from 0)
+    it.begin[i] = it.first + (it.lo[i] <= a.sinks ? 0 : (it.lo[i] - it.start) / kKeys);
+    it.last[i] = it.hi[i] > 0 ? it.first + (it.hi[i] - 1 - it.start) / kKeys : -1;
+  }
   return it;
 }
 
-// Maximum of a row of 128 scores held as raw fp32 bits, in eight independent chains.
-__device__ __forceinline__ float row_max128(const uint32_t (&r)[4][32]) {
-  float m[8];
+// Maximum of 32 scores held as raw fp32 bits, in two independent chains.
+__device__ __forceinline__ float max32(const uint32_t (&r)[32]) {
+  float m[2];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t* v = &r[k >> 1][(k & 1) * 16];
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t* v = &r[k * 16];
     m[k] = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
 #pragma unroll
     for (int i = 2; i < 16; i += 2) m[k] = max3f(m[k], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
   }
-  return max3f(max3f(m[0], m[1], m[2]), max3f(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
+  return fmaxf(m[0], m[1]);
+}
+
+// 32 bytes in one store (p 32-byte aligned).
+__device__ __forceinline__ void st_global32(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
 }
 
 // Bits [lo, hi) of a 32-bit word (both clamped to it).
@@ -146,53 +177,233 @@ __device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
   return below_hi & ~below_lo;
 }
 
+// Waits (a short time, so without sleep) until a counter in shared memory has reached `need`. A
+// whole warp; the bound is checked every 64 polls.
+__device__ __forceinline__ bool wait_count(volatile uint32_t* count, uint32_t need, const WaitGuard& g) {
+  uint64_t t0 = 0;
+  for (uint32_t spin = 1; !__all_sync(0xffffffffu, *count >= need); ++spin) {
+    if ((spin & 63) != 0) continue;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (__any_sync(0xffffffffu, *g.abort != 0 || now - t0 > g.limit_ns)) return false;
+  }
+  return true;
+}
+
+// Where everything is in shared memory.
+template <int HD>
+struct Shared {
+  using L = Layout<HD>;
+  uint8_t *q, *k, *v;            // Q0 Q1, K [kStagesK], V [kStagesV]
+  uint64_t *q_full, *q_empty;    // [2] Q_i has landed; the item's last S_i has read it
+  uint64_t *s_full, *s_free;     // [2] S_i is in its columns; it has been read out of them
+  uint64_t *p_full, *pv_done;    // [2] P_i is in place (and O_i rescaled); P_i V is in O_i
+  uint64_t* drains;              // [2] wind-down of the issuers
+  volatile uint32_t* s_issued;   // [2] S products issued for a slot
+  uint64_t *k_full, *k_empty, *v_full, *v_empty;  // per stage: a tile has landed; its last user is done with it
+  uint64_t *item_full, *item_empty;               // [kItems] a work item is published; every role is done with it
+  volatile int* abort_flag;
+  uint32_t* tmem_slot;
+  Item* items;                   // [kItems]
+
+  __device__ explicit Shared(uint8_t* base) {
+    constexpr int NK = L::kStagesK, NV = L::kStagesV;
+    q = base;
+    k = base + 2 * L::kQB;
+    v = k + NK * L::kKB;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(v + NV * L::kKB);
+    q_full = bars;
+    q_empty = bars + 2;
+    s_full = bars + 4;
+    s_free = bars + 6;
+    p_full = bars + 8;
+    pv_done = bars + 10;
+    drains = bars + 12;
+    s_issued = reinterpret_cast<volatile uint32_t*>(bars + 14);
+    k_full = bars + 16;
+    k_empty = k_full + NK;
+    v_full = k_full + 2 * NK;
+    v_empty = v_full + NV;
+    item_full = v_full + 2 * NV;
+    item_empty = item_full + kItems;
+    abort_flag = reinterpret_cast<volatile int*>(item_empty + kItems);
+    tmem_slot = reinterpret_cast<uint32_t*>(item_empty + kItems) + 1;
+    items = reinterpret_cast<Item*>(reinterpret_cast<uint8_t*>(bars) + 512);
+    static_assert((16 + 2 * NK + 2 * NV + 2 * kItems) * 8 + 8 <= 512 && 512 + kItems * sizeof(Item) <= L::kCtrlB,
+                  "control block");
+  }
+};
+
+// S = Q K^T for slot 0 and slot 1 in turn, tile by tile, each as soon as its buffer has been read.
+// A whole warp walks the tiles in step; one of its lanes issues.
+template <int HD>
+__device__ __forceinline__ void issue_scores(const Shared<HD>& sm, const WaitGuard& guard, uint32_t tmem) {
+  using L = Layout<HD>;
+  constexpr uint32_t IDESC_S = idesc_bf16(128, 0, false, false);  // + columns / 8 << 17
+  const uint32_t one = elect_one();
+  const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(sm.q)), k_desc = sdesc_kmajor_sw128(smem_u32(sm.k));
+  uint32_t stage = 0, par = 0, n0 = 0, n1 = 0;  // K stage and its parity, S products of each slot so far
+  bool ok = true;
+  for (int k = 0; ok; ++k) {
+    if (!(ok = mbar_sleep_warp(&sm.item_full[k % kItems], (k / kItems) & 1, guard))) break;
+    const Item& it = sm.items[k % kItems];
+    const int count = __shfl_sync(0xffffffffu, it.count, 0);
+    if (count == 0) break;
+    for (int x = 0; ok && x < count; ++x) {
+      if (!(ok = mbar_sleep_warp(&sm.k_full[stage], par, guard))) break;
+      const bool both = __shfl_sync(0xffffffffu, it.uses(0, x) && it.uses(1, x), 0);
+      const int from = __shfl_sync(0xffffffffu, it.uses(0, x) ? 0 : 1, 0), to = both ? 2 : from + 1;
+#pragma unroll 1
+      for (int i = from; i < to; ++i) {
+        const int cols = __shfl_sync(0xffffffffu, it.cols(i, x), 0);
+        const uint32_t mine = i ? n1 : n0, before = L::kSharedS ? n0 + n1 : mine;
+        // (the slot's k-th item has its queries in the k-th filling that it took part in)
+        if (x == __shfl_sync(0xffffffffu, it.first_used(i), 0) &&
+            !(ok = mbar_sleep_warp(&sm.q_full[i], __shfl_sync(0xffffffffu, it.nth[i], 0) & 1, guard)))
+          break;
+        // the scores before it have been read out of the buffer
+        if (before > 0 && !(ok = mbar_sleep_warp(&sm.s_free[L::kSharedS ? 0 : i], (before - 1) & 1, guard))) break;
+        if (i)
+          ++n1;
+        else
+          ++n0;
+        tc_fence_after();
+        const uint64_t qd = q_desc + i * (L::kQB / 16), kd = k_desc + stage * (L::kKB / 16);
+        const uint32_t idesc = IDESC_S | (static_cast<uint32_t>(cols) >> 3 << 17), d = tmem + L::col_s(i);
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk)
+          umma_ss_one(one, d, qd + (kk >> 2) * (L::kBox / 16) + (kk & 3) * 2,
+                      kd + (kk >> 2) * (L::kBox / 16) + (kk & 3) * 2, idesc, kk > 0);
+        umma_commit_one(one, &sm.s_full[i]);
+        if (one) sm.s_issued[i] = mine + 1;
+        if (i + 1 == to) umma_commit_one(one, &sm.k_empty[stage]);
+        if (x == __shfl_sync(0xffffffffu, it.last[i], 0)) umma_commit_one(one, &sm.q_empty[i]);
+      }
+      if (++stage == L::kStagesK) {
+        stage = 0;
+        par ^= 1;
+      }
+    }
+    __syncwarp();
+    if (one) mbar_arrive(&sm.item_empty[k % kItems]);
+  }
+  if (!ok) give_up(guard);
+  if (*guard.abort) {
+    umma_commit_one(one, &sm.drains[0]);
+    if (one) drain_wait(&sm.drains[0], 0);
+  }
+  __syncwarp();
+}
+
+// O += P V in the same order, by a warp of its own (its lanes clear the rows of V past a clip's
+// end). The tensor core runs products in the order they are issued: a slot's next S, which its
+// softmax waits for, goes ahead of its P V.
+template <int HD>
+__device__ __forceinline__ void issue_outputs(const WindowArgs& args, const Shared<HD>& sm, const WaitGuard& guard,
+                                              uint32_t tmem) {
+  using L = Layout<HD>;
+  constexpr uint32_t IDESC_O = idesc_bf16(128, HD, false, true);
+  const uint32_t lane = threadIdx.x & 31, one = elect_one();
+  const uint64_t v_desc = sdesc_mnmajor_sw128(smem_u32(sm.v), L::kBox);
+  uint32_t stage = 0, par = 0, n0 = 0, n1 = 0;  // V stage and its parity, P V products of each slot so far
+  bool ok = true;
+  for (int k = 0; ok; ++k) {
+    if (!(ok = mbar_sleep_warp(&sm.item_full[k % kItems], (k / kItems) & 1, guard))) break;
+    const Item& it = sm.items[k % kItems];
+    const int count = __shfl_sync(0xffffffffu, it.count, 0);
+    if (count == 0) break;
+    for (int x = 0; ok && x < count; ++x) {
+      if (!(ok = mbar_sleep_warp(&sm.v_full[stage], par, guard))) break;
+      const int clear = __shfl_sync(0xffffffffu, it.n < args.T ? it.n - it.base(x) : kKeys, 0);
+      if (clear < kKeys) {
+        // rows past the clip's length hold anything (NaN times a weight of zero is NaN): zeros
+        for (int r = clear + (lane >> 3); r < kKeys; r += 4)
+          for (int b = 0; b < L::kBoxes; ++b)
+            *reinterpret_cast<uint4*>(sm.v + stage * L::kKB + b * L::kBox + r * 128 + (lane & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      const bool both = __shfl_sync(0xffffffffu, it.uses(0, x) && it.uses(1, x), 0);
+      const int from = __shfl_sync(0xffffffffu, it.uses(0, x) ? 0 : 1, 0), to = both ? 2 : from + 1;
+#pragma unroll 1
+      for (int i = from; i < to; ++i) {
+        const int cols = __shfl_sync(0xffffffffu, it.cols(i, x), 0);
+        const bool adds = __shfl_sync(0xffffffffu, x != it.first_used(i), 0);
+        const uint32_t mine = i ? n1 : n0;
+        if (!(ok = mbar_sleep_warp(&sm.p_full[i], mine & 1, guard))) break;
+        if (x != __shfl_sync(0xffffffffu, it.last[i], 0) && !(ok = wait_count(&sm.s_issued[i], mine + 2, guard))) break;
+        if (i)
+          ++n1;
+        else
+          ++n0;
+        tc_fence_after();
+        const uint64_t vd = v_desc + stage * (L::kKB / 16);
+        const uint32_t d = tmem + L::col_o(i), pa = tmem + L::col_p(i);
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          if (kk * 16 < cols) umma_ts_one(one, d, pa + kk * 8, vd + kk * (2048 / 16), IDESC_O, (adds || kk > 0));
+        umma_commit_one(one, &sm.pv_done[i]);
+        if (i + 1 == to) umma_commit_one(one, &sm.v_empty[stage]);
+      }
+      if (++stage == L::kStagesV) {
+        stage = 0;
+        par ^= 1;
+      }
+    }
+    __syncwarp();
+    if (one) mbar_arrive(&sm.item_empty[k % kItems]);
+  }
+  if (!ok) give_up(guard);
+  if (*guard.abort) {
+    umma_commit_one(one, &sm.drains[1]);
+    if (one) drain_wait(&sm.drains[1], 0);
+  }
+  __syncwarp();
+}
+
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
     window_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const WindowArgs args) {
   using L = Layout<HD>;
-  constexpr int TB = L::kTileB, NS = L::kStages;
+  constexpr int NK = L::kStagesK, NV = L::kStagesV;
   extern __shared__ unsigned char smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sQ = smem;                // Q0, Q1
-  uint8_t* sK = smem + 2 * TB;       // [NS]
-  uint8_t* sV = sK + NS * TB;        // [NS]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + NS * TB);
-  uint64_t* q_full = bars;           // [2] Q_i has landed
-  uint64_t* q_empty = bars + 2;      // [2] the item's last S_i has read Q_i
-  uint64_t* s_full = bars + 4;       // [2] S_i is in its buffer
-  uint64_t* s_free = bars + 6;       // [2] a buffer has been read ([0] alone where it is shared)
-  uint64_t* p_full = bars + 8;       // [2] P_i is stored and O_i rescaled
-  uint64_t* pv_done = bars + 10;     // [2] P_i V is in O_i
-  uint64_t* drains = bars + 12;      // [2] wind-down of the issuers
-  uint64_t* k_full = bars + 14;      // [NS]
-  uint64_t* k_empty = k_full + NS;
-  uint64_t* v_full = k_full + 2 * NS;
-  uint64_t* v_empty = k_full + 3 * NS;
-  volatile int* s_issued = reinterpret_cast<volatile int*>(k_full + 4 * NS);  // [2] S products issued per slot
-  volatile int* abort_flag = s_issued + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(const_cast<int*>(s_issued) + 3);
-  int* lens = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 512);
-  static_assert((14 + 4 * NS) * 8 + 16 <= 512, "barriers");
+  const Shared<HD> sm(smem);
+  uint64_t *const q_full = sm.q_full, *const q_empty = sm.q_empty, *const s_full = sm.s_full, *const s_free = sm.s_free;
+  uint64_t *const p_full = sm.p_full, *const pv_done = sm.pv_done, *const k_full = sm.k_full, *const k_empty = sm.k_empty;
+  uint64_t *const v_full = sm.v_full, *const v_empty = sm.v_empty, *const item_full = sm.item_full;
+  uint64_t* const item_empty = sm.item_empty;
+  uint8_t *const sQ = sm.q, *const sK = sm.k, *const sV = sm.v;
+  volatile int* const abort_flag = sm.abort_flag;
+  uint32_t* const tmem_slot = sm.tmem_slot;
+  Item* const items = sm.items;
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
   const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&s_free[i], 4);  // one arrival per warp of the slot that read it
-      mbar_init(&p_full[i], 128);
+      mbar_init(&s_free[i], 4);  // one arrival per softmax warp of the slot
+      mbar_init(&p_full[i], 4);
       mbar_init(&pv_done[i], 1);
-      mbar_init(&drains[i], 1);
-      s_issued[i] = 0;
+      mbar_init(&sm.drains[i], 1);
+      sm.s_issued[i] = 0;
     }
-    for (int s = 0; s < NS; ++s) {
+    for (int s = 0; s < NK; ++s) {
       mbar_init(&k_full[s], 1);
       mbar_init(&k_empty[s], 1);
+    }
+    for (int s = 0; s < NV; ++s) {
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&item_full[i], 1);
+      mbar_init(&item_empty[i], 11);  // loader, two issuers, eight softmax warps
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -204,198 +415,146 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  pdl_wait();
-  pdl_trigger();
-  if (args.lengths)
-    for (int i = threadIdx.x; i < min(args.batch, kLengths); i += kThreads) lens[i] = *SAL_CK_LD(args.lengths + i, 4);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  pdl_wait();
+  pdl_trigger();
   const uint32_t tmem = *tmem_slot;
   const WaitGuard guard{abort_flag, args.limit_ns, args.status};
-  // the producer's record of what it has loaded, for the wind-down
+  // the loaders' records of what they have loaded, for the wind-down
   uint32_t loads_q[2] = {0, 0}, loads_k = 0, loads_v = 0;
   bool ok = true;
+  // Waits for the k-th work item of this block; done_with lets its place be reused.
+  auto item_ready = [&](int k) { return mbar_sleep(&item_full[k % kItems], (k / kItems) & 1, guard); };
+  auto done_with = [&](int k) { mbar_arrive(&item_empty[k % kItems]); };
+
   // Each role runs inside the branch that set its register limit.
   if (warp < 4) {
     setmaxnreg_dec<kRegsCtrl>();
-    if (warp == 0 && lane == 0) {
-      for (int idx = blockIdx.x; ok && idx < args.items; idx += gridDim.x) {
-        const Item it = item_of(args, idx, lens);
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int k = 0; ok; ++k) {
+        if (!(ok = item_ready(k))) break;
+        const Item& it = items[k % kItems];
+        if (it.count == 0) break;
         for (int x = 0; ok && x < it.count; ++x) {
-          const uint32_t s = loads_k % NS, par = (loads_k / NS) & 1;
-          const int row = it.tile(x) * kTile;
-          if (!(ok = mbar_wait(&k_empty[s], par ^ 1, guard))) break;
-          mbar_arrive_expect_tx(&k_full[s], TB);
-          for (int b = 0; b < L::kBoxes; ++b) tma_load_3d(sK + s * TB + b * kBox, &tmK, &k_full[s], 64 * b, row, it.kv);
+          const uint32_t sk = loads_k % NK, sv = loads_v % NV;
+          const int row = it.base(x);
+          if (!(ok = mbar_sleep(&k_empty[sk], ((loads_k / NK) & 1) ^ 1, guard))) break;
+          mbar_arrive_expect_tx(&k_full[sk], L::kKB);
+          for (int b = 0; b < L::kBoxes; ++b)
+            tma_load_3d(sK + sk * L::kKB + b * L::kBox, &tmK, &k_full[sk], 64 * b, row, it.kv);
           ++loads_k;
-          // an item's queries behind its first key tile, which the ring could take earlier
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (x > 0 || !ok || it.hi[i] == 0) continue;
-            if (!(ok = mbar_wait(&q_empty[i], (loads_q[i] & 1) ^ 1, guard))) continue;
-            mbar_arrive_expect_tx(&q_full[i], TB);
-            for (int b = 0; b < L::kBoxes; ++b)
-              tma_load_3d(sQ + i * TB + b * kBox, &tmQ, &q_full[i], 64 * b, it.row[i], it.b * args.heads + it.head[i]);
-            ++loads_q[i];
-          }
-          if (!ok || !(ok = mbar_wait(&v_empty[s], par ^ 1, guard))) break;
-          mbar_arrive_expect_tx(&v_full[s], TB);
-          for (int b = 0; b < L::kBoxes; ++b) tma_load_3d(sV + s * TB + b * kBox, &tmV, &v_full[s], 64 * b, row, it.kv);
+          if (!(ok = mbar_sleep(&v_empty[sv], ((loads_v / NV) & 1) ^ 1, guard))) break;
+          mbar_arrive_expect_tx(&v_full[sv], L::kKB);
+          for (int b = 0; b < L::kBoxes; ++b)
+            tma_load_3d(sV + sv * L::kKB + b * L::kBox, &tmV, &v_full[sv], 64 * b, row, it.kv);
           ++loads_v;
         }
-      }
-    } else if (warp == 1 && lane == 0) {
-      constexpr uint32_t IDESC_S = idesc_bf16(128, 128, false, false);
-      uint32_t n_k = 0, n_s[2] = {0, 0}, n_q[2] = {0, 0};
-      for (int idx = blockIdx.x; ok && idx < args.items; idx += gridDim.x) {
-        const Item it = item_of(args, idx, lens);
-        bool begun[2] = {false, false};
-        for (int x = 0; ok && x < it.count; ++x) {
-          const uint32_t s = n_k % NS;
-          if (!(ok = mbar_wait(&k_full[s], (n_k / NS) & 1, guard))) break;
-          ++n_k;
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (!ok || !it.uses(i, x)) continue;
-            if (!begun[i]) {
-              if (!(ok = mbar_wait(&q_full[i], n_q[i] & 1, guard))) continue;
-              ++n_q[i];
-              begun[i] = true;
-            }
-            // the buffer's last scores have been read out of it
-            const uint32_t before = L::kSharedS ? n_s[0] + n_s[1] : n_s[i];
-            if (before > 0 && !(ok = mbar_wait(&s_free[L::kSharedS ? 0 : i], (before - 1) & 1, guard)))
-              continue;
-            tc_fence_after();
-            const uint32_t q0 = smem_u32(sQ + i * TB), k0 = smem_u32(sK + s * TB);
-#pragma unroll
-            for (int kk = 0; kk < HD / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
-              umma_ss(tmem + L::col_s(i), sdesc_kmajor_sw128(q0 + off), sdesc_kmajor_sw128(k0 + off), IDESC_S, kk > 0);
-            }
-            umma_commit(&s_full[i]);
-            s_issued[i] = ++n_s[i];
-            if (x == it.last(i)) umma_commit(&q_empty[i]);
-          }
-          if (ok) umma_commit(&k_empty[s]);
-        }
-      }
-      if (*abort_flag) {
-        umma_commit(&drains[0]);
-        drain_wait(&drains[0], 0);
-      }
-    } else if (warp == 2) {
-      constexpr uint32_t IDESC_O = idesc_bf16(128, HD, false, true);
-      uint32_t n_v = 0, n_p[2] = {0, 0};
-      for (int idx = blockIdx.x; ok && idx < args.items; idx += gridDim.x) {
-        const Item it = item_of(args, idx, lens);
-        bool begun[2] = {false, false};
-        for (int x = 0; ok && x < it.count; ++x) {
-          const uint32_t s = n_v % NS;
-          if (lane == 0) ok = mbar_wait(&v_full[s], (n_v / NS) & 1, guard);
-          if (!(ok = __shfl_sync(0xffffffffu, ok, 0))) break;
-          ++n_v;
-          const int base = it.tile(x) * kTile;
-          if (base + kTile > it.n && it.n < args.T) {
-            // rows past the clip's length hold anything (NaN times a weight of zero is NaN): zeros
-            __syncwarp();
-            for (int r = it.n - base + (lane >> 3); r < kTile; r += 4)
-              for (int b = 0; b < L::kBoxes; ++b)
-                *reinterpret_cast<uint4*>(sV + s * TB + b * kBox + r * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          if (lane == 0) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (!ok || !it.uses(i, x)) continue;
-              if (!(ok = mbar_wait(&p_full[i], n_p[i] & 1, guard))) continue;
-              if (x != it.last(i)) {
-                // the tensor core runs products in the order they are issued: the slot's next S, which
-                // its softmax waits for, goes ahead of this product. A short spin, its bound checked
-                // every 64 polls.
-                const int need = static_cast<int>(n_p[i]) + 2;
-                uint64_t t0 = 0;
-                for (uint32_t spin = 1; s_issued[i] < need; ++spin) {
-                  if ((spin & 63) != 0) continue;
-                  if (*abort_flag) {
-                    ok = false;
-                    break;
-                  }
-                  const uint64_t now = globaltimer_ns();
-                  if (t0 == 0) {
-                    t0 = now;
-                  } else if (now - t0 > args.limit_ns) {
-                    *abort_flag = 1;
-                    atomicOr(args.status, kStatusTimeout);
-                    ok = false;
-                    break;
-                  }
-                }
-                if (!ok) continue;
-              }
-              tc_fence_after();
-              const uint32_t v0 = smem_u32(sV + s * TB);
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                umma_ts(tmem + L::col_o(i), tmem + L::col_p(i) + kk * 8, sdesc_mnmajor_sw128(v0 + kk * 2048, kBox),
-                        IDESC_O, (begun[i] || kk > 0));
-              umma_commit(&pv_done[i]);
-              begun[i] = true;
-              ++n_p[i];
-            }
-            if (ok) umma_commit(&v_empty[s]);
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-        }
-      }
-      if (lane == 0 && *abort_flag) {
-        umma_commit(&drains[1]);
-        drain_wait(&drains[1], 0);
+        done_with(k);
       }
     }
+  } else if (warp == 1) {
+    issue_scores<HD>(sm, guard, tmem);
+  } else if (warp == 2) {
+    issue_outputs<HD>(args, sm, guard, tmem);
+  } else if (warp == 3) {
+    if (lane == 0) {
+      // works the items out one ahead of the other roles (those past a clip's end are left out, an
+      // item of no tiles is the end), and loads their queries as soon as a slot's last S has read
+      // the ones before
+      int idx = blockIdx.x;
+      int nth[2] = {0, 0};
+      auto publish = [&](int k) {
+        Item it;
+        it.count = 0;
+        for (; idx < args.items; idx += gridDim.x) {
+          it = item_of(args, idx);
+          if (it.count > 0) break;
+        }
+        idx += gridDim.x;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          it.nth[i] = nth[i];
+          nth[i] += it.count > 0 && it.hi[i] > 0;
+        }
+        if ((ok = mbar_sleep(&item_empty[k % kItems], ((k / kItems) & 1) ^ 1, guard))) {
+          items[k % kItems] = it;
+          mbar_arrive(&item_full[k % kItems]);
+        }
+        return it;
+      };
+      Item now = publish(0);
+      for (int k = 0; ok && now.count > 0; ++k) {
+        const Item next = publish(k + 1);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (!ok || now.hi[i] == 0) continue;
+          if (!(ok = mbar_sleep(&q_empty[i], (loads_q[i] & 1) ^ 1, guard))) continue;
+          mbar_arrive_expect_tx(&q_full[i], L::kQB);
+          for (int b = 0; b < L::kBoxes; ++b)
+            tma_load_3d(sQ + i * L::kQB + b * L::kBox, &tmQ, &q_full[i], 64 * b, now.row[i],
+                        now.b * args.heads + now.head[i]);
+          ++loads_q[i];
+        }
+        now = next;
+      }
+    }
+  }
   } else {
     setmaxnreg_inc<kRegsSoftmax>();
-    const int wg = (warp - 4) >> 2;  // slot
-    const int quarter = warp & 3;
+    const int slot = (warp - 4) >> 2, quarter = warp & 3;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t colS = L::col_s(wg), colO = L::col_o(wg), colP = L::col_p(wg);
+    const uint32_t colS = tmem + lane_base + L::col_s(slot), colP = tmem + lane_base + L::col_p(slot);
+    const uint32_t colO = tmem + lane_base + L::col_o(slot);
     const int row = quarter * 32 + lane;
     const float sl2 = args.scale_log2;
     uint32_t n_s = 0;  // score tiles of this slot so far
-    for (int idx = blockIdx.x; ok && idx < args.items; idx += gridDim.x) {
-      const Item it = item_of(args, idx, lens);
-      if (it.hi[wg] == 0) continue;
-      const int p = it.row[wg] + row;
-      const int key_lo = max(0, p - args.left), key_hi = min(it.n, p + args.right + 1), key_sink = min(args.sinks, key_hi);
+    for (int k = 0; ok; ++k) {
+      if (!(ok = mbar_sleep_warp(&item_full[k % kItems], (k / kItems) & 1, guard))) break;
+      const Item& it = items[k % kItems];
+      if (it.count == 0) break;
+      const int p = it.row[slot] + row;
+      const int key_lo = max(0, p - args.left), key_hi = min(it.n, p + args.right + 1);
       float m_ref = -INFINITY, l = 0.f;
       bool begun = false;
-      for (int x = 0; x < it.count; ++x) {
-        if (!it.uses(wg, x)) continue;
-        if (!(ok = mbar_wait_warp(&s_full[wg], n_s & 1, guard))) break;
+      const int last = it.last[slot], first = it.first;
+      for (int x = it.first_used(slot); x <= last; x = it.next_used(slot, x)) {
+        if (!(ok = mbar_sleep_warp(&s_full[slot], n_s & 1, guard))) break;
         tc_fence_after();
-        // the whole row of scores in registers, then the buffer goes back to the tensor core
         uint32_t r[4][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lane_base + colS + 32 * c, r[c]);
+        for (int c = 0; c < 4; ++c) tmem_ld32(colS + 32 * c, r[c]);
+        const int base = it.base(x);
+        const int c_lo = x < first ? 0 : key_lo - base, c_hi = x < first ? 0 : key_hi - base;
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&s_free[L::kSharedS ? 0 : wg]);
-        const int base = it.tile(x) * kTile;
-        const int c_hi = key_hi - base, c_sink = key_sink - base;
-        const int c_lo = c_sink >= key_lo - base ? 0 : key_lo - base;  // first positions that reach the window
-        if (!__all_sync(0xffffffffu, c_hi >= kTile && c_lo <= 0)) {
+        if (lane == 0) mbar_arrive(&s_free[L::kSharedS ? 0 : slot]);  // back to the tensor core
+        // 32-column chunks that some row of the warp sees (the others cost nothing below)
+        uint32_t live = 15u;
+        if (!__all_sync(0xffffffffu, c_hi >= kKeys && c_lo <= 0)) {
+          const int c_sink = min(args.sinks, key_hi) - base;
+          live = 0;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const uint32_t seen = bits_between(c_lo - 32 * c, c_hi - 32 * c) | bits_between(0, c_sink - 32 * c);
+            if (__any_sync(0xffffffffu, seen != 0)) {
+              live |= 1u << c;
+              if (!__all_sync(0xffffffffu, seen == 0xffffffffu)) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((seen >> i) & 1u)) r[c][i] = 0xff800000u;  // -inf
+                for (int i = 0; i < 32; ++i)
+                  if (!((seen >> i) & 1u)) r[c][i] = 0xff800000u;  // -inf
+              }
+            }
           }
         }
-        const float mx = row_max128(r) * sl2;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if ((live >> c) & 1u) mx = fmaxf(mx, max32(r[c]));
+        mx *= sl2;
         float alpha = 1.f;
         bool rescale = false;
         if (!begun) {
@@ -410,72 +569,83 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t sum2[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
+          sum2[c] = 0;
+          if ((live >> c) & 1u) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            float x0, x1, e0, e1;
-            f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1])), sl2_2, negm_2), x0, x1);
-            if (HD == 64 && ((i >> 1) & 15) < 6) {
-              exp2_pair_poly(x0, x1, e0, e1);
-            } else {
-              e0 = fast_exp2(x0);
-              e1 = fast_exp2(x1);
+            for (int i = 0; i < 32; i += 2) {
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1])), sl2_2, negm_2), x0, x1);
+              const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+              sum2[c] = i == 0 ? f2_pack(e0, e1) : f2_add(sum2[c], f2_pack(e0, e1));
+              r[c >> 1][(c & 1) * 16 + (i >> 1)] = pack_bf16x2(e0, e1);
             }
-            sum2[c] = i == 0 ? f2_pack(e0, e1) : f2_add(sum2[c], f2_pack(e0, e1));
-            r[c >> 1][(c & 1) * 16 + (i >> 1)] = pack_bf16x2(e0, e1);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[c >> 1][(c & 1) * 16 + i] = 0;
           }
         }
-        if (begun) {
+        if (n_s > 0) {
           // P V of the tile before must be complete before O is rescaled or P overwritten
-          if (!(ok = mbar_wait_warp(&pv_done[wg], (n_s - 1) & 1, guard))) break;
+          if (!(ok = mbar_sleep_warp(&pv_done[slot], (n_s - 1) & 1, guard))) break;
           tc_fence_after();
         }
-        tmem_st32(tmem + lane_base + colP, r[0]);
-        tmem_st32(tmem + lane_base + colP + 32, r[1]);
+        tmem_st32(colP, r[0]);
+        tmem_st32(colP + 32, r[1]);
         if (begun && __any_sync(0xffffffffu, rescale)) {
 #pragma unroll 1
           for (int c = 0; c < HD / 32; ++c) {
             uint32_t o[32];
-            tmem_ld32(tmem + lane_base + colO + 32 * c, o);
+            tmem_ld32(colO + 32 * c, o);
             tmem_wait_ld();
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-            tmem_st32(tmem + lane_base + colO + 32 * c, o);
+            tmem_st32(colO + 32 * c, o);
           }
         }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[slot]);
         float sum_lo, sum_hi;
         f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), sum_lo, sum_hi);
         l = l * alpha + (sum_lo + sum_hi);
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&p_full[wg]);
         begun = true;
         ++n_s;
       }
-      if (!ok || !(ok = mbar_wait_warp(&pv_done[wg], (n_s - 1) & 1, guard))) break;
+      if (!ok) break;
+      const bool stored = p < it.n;
+      __nv_bfloat16* dst = args.o + ((static_cast<int64_t>(it.b) * args.T + p) * args.heads + it.head[slot]) * HD;
+      __syncwarp();
+      if (lane == 0) done_with(k);
+      if (!begun) continue;  // an empty slot
+      if (!(ok = mbar_sleep_warp(&pv_done[slot], (n_s - 1) & 1, guard))) break;
       tc_fence_after();
       const float inv_l = 1.0f / l;
-      __nv_bfloat16* dst = args.o + ((static_cast<int64_t>(it.b) * args.T + p) * args.heads + it.head[wg]) * HD;
 #pragma unroll 1
       for (int c = 0; c < HD / 32; ++c) {
-        uint32_t o[32];
-        tmem_ld32(tmem + lane_base + colO + 32 * c, o);
+        uint32_t u[32];
+        tmem_ld32(colO + 32 * c, u);
         tmem_wait_ld();
-        if (p < it.n) {
-          uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * c);
+        if (stored) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint4 u;
-            u.x = pack_bf16x2(__uint_as_float(o[8 * i + 0]) * inv_l, __uint_as_float(o[8 * i + 1]) * inv_l);
-            u.y = pack_bf16x2(__uint_as_float(o[8 * i + 2]) * inv_l, __uint_as_float(o[8 * i + 3]) * inv_l);
-            u.z = pack_bf16x2(__uint_as_float(o[8 * i + 4]) * inv_l, __uint_as_float(o[8 * i + 5]) * inv_l);
-            u.w = pack_bf16x2(__uint_as_float(o[8 * i + 6]) * inv_l, __uint_as_float(o[8 * i + 7]) * inv_l);
-            *SAL_CK_ST(d4 + i, 16) = u;
+          for (int i = 0; i < 16; ++i)
+            u[i] = pack_bf16x2(__uint_as_float(u[2 * i]) * inv_l, __uint_as_float(u[2 * i + 1]) * inv_l);
+          if (args.wide) {  // a whole 32-byte sector at a time
+#pragma unroll
+            for (int i = 0; i < 2; ++i) st_global32(SAL_CK_ST(dst + 32 * c + 16 * i, 32), &u[8 * i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *SAL_CK_ST(reinterpret_cast<uint4*>(dst + 32 * c) + i, 16) =
+                  make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
           }
         }
       }
+      // (O is overwritten by the next item's first product, which waits for this slot's next P)
     }
   }
 
+  if (!ok) give_up(guard);
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -485,13 +655,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // Every role has finished, so the abort flag is final: let every load this block issued land
   // before the block, and its shared memory, goes away.
-  if (warp == 0 && lane == 0 && *abort_flag) {
+  if ((warp == 0 || warp == 3) && lane == 0 && *abort_flag) {
     for (int i = 0; i < 2; ++i)
       if (loads_q[i] > 0) drain_wait(&q_full[i], (loads_q[i] - 1) & 1);
-    for (uint32_t s = 0; s < NS; ++s) {  // the last load of stage s: the largest j < loads with j % NS == s
-      if (loads_k > s) drain_wait(&k_full[s], ((loads_k - 1 - s) / NS) & 1);
-      if (loads_v > s) drain_wait(&v_full[s], ((loads_v - 1 - s) / NS) & 1);
-    }
+    // the last load of stage s: the largest j < loads with j % stages == s
+    for (uint32_t s = 0; s < NK; ++s)
+      if (loads_k > s) drain_wait(&k_full[s], ((loads_k - 1 - s) / NK) & 1);
+    for (uint32_t s = 0; s < NV; ++s)
+      if (loads_v > s) drain_wait(&v_full[s], ((loads_v - 1 - s) / NV) & 1);
   }
 }
 
@@ -503,12 +674,10 @@ bool prepare_kernel() {
   cudaFuncAttributes fa{};
   return cudaFuncSetAttribute(window_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               static_cast<int>(Layout<HD>::kSmem)) == cudaSuccess &&
-         cudaFuncGetAttributes(&fa, window_kernel<HD>) == cudaSuccess && fa.numRegs * kThreads >= kRegsNeeded &&
-         fa.numRegs <= 168;
+         cudaFuncGetAttributes(&fa, window_kernel<HD>) == cudaSuccess && fa.numRegs == kRegsLaunch;
 }
 
-// SMs of the current device once both kernels may run on it (their launch registers must cover
-// the split between the warpgroups); 0 if not.
+// SMs of the current device once both kernels may run on it; 0 if not.
 int ready_sms() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
@@ -542,6 +711,7 @@ sal_status window_attention_launch(const void* q, const void* k, const void* v, 
   a.right = win.right < 0 ? a.T : static_cast<int>(std::min<int64_t>(win.right, T));
   a.sinks = static_cast<int>(std::min<int64_t>(win.sinks, T));
   a.tiles = (a.T + kTile - 1) / kTile;
+  a.wide = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(head_dim));
   a.limit_ns = wait_limit_ns();
   a.status = device_status_ptr();
@@ -561,8 +731,8 @@ sal_status window_attention_launch(const void* q, const void* k, const void* v, 
   const uint64_t hd = static_cast<uint64_t>(head_dim), rows = static_cast<uint64_t>(T);
   const uint64_t kvp = static_cast<uint64_t>(batch) * kv_heads;
   if (!make_tmap_3d_bf16(&tq, q, hd, rows, static_cast<uint64_t>(planes), 64, kTile, 1) ||
-      !make_tmap_3d_bf16(&tk, k, hd, rows, kvp, 64, kTile, 1) ||
-      !make_tmap_3d_bf16(&tv, v, hd, rows, kvp, 64, kTile, 1))
+      !make_tmap_3d_bf16(&tk, k, hd, rows, kvp, 64, kKeys, 1) ||
+      !make_tmap_3d_bf16(&tv, v, hd, rows, kvp, 64, kKeys, 1))
     return SAL_ECUDA;
   ck_declare(o, static_cast<uint64_t>(planes) * rows * hd * 2, true);
   ck_declare(lengths, static_cast<uint64_t>(batch) * 4, false);

@@ -75,11 +75,15 @@ def test_lengths_and_what_lies_past_them(T, H, kvh, d, left, right, sinks):
     rows = o.reshape(B, T, H * d)
     for b, n in enumerate(lens):
         assert bool((rows[b, max(0, min(n, T)):] == 7.0).all()), b
-    # a clip's result does not depend on the padding around it
+    # what lies past the lengths is not used: other padding, the same bits
+    again = torch.full_like(o, 7.0)
+    api.sal_attention_window(*clean, left=left, right=right, sinks=sinks,
+                             lengths=torch.tensor(lens, dtype=torch.int32, device="cuda"), out=again)
+    assert torch.equal(o, again)
+    # and a clip alone, whose keys may fall into other tiles, agrees within the bound
     for b in (3, 4, 5):
-        alone = api.sal_attention_window(*(x[b:b + 1, :, :lens[b]].contiguous() for x in clean), left=left,
-                                         right=right, sinks=sinks)
-        assert torch.equal(rows[b, :lens[b]], alone)
+        alone = [x[b:b + 1, :, :lens[b]].contiguous() for x in clean]
+        _compare(api.sal_attention_window(*alone, left=left, right=right, sinks=sinks), *alone, left, right, sinks)
 
 
 @pytest.mark.parametrize("d", [64, 128])
