@@ -71,6 +71,18 @@ __device__ __forceinline__ bool mbar_sleep_once(uint64_t* bar, uint32_t parity) 
       : "memory");
   return ok != 0;
 }
+// Whether the phase is complete, without waiting for it.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity, const WaitGuard& g) {
   if (mbar_sleep_once(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();

@@ -92,13 +92,6 @@ struct Item {
   int nth[2];           // items that a slot took part in before this one
 
   __device__ int base(int x) const { return x < first ? kKeys * x : start + kKeys * (x - first); }
-  __device__ bool uses(int i, int x) const { return x <= last[i] && (x < first || x >= begin[i]); }
-  __device__ int first_used(int i) const { return first > 0 ? 0 : begin[i]; }
-  __device__ int next_used(int i, int x) const { return x + 1 == first ? begin[i] : x + 1; }
-  // keys of tile x that the slot multiplies with: a multiple of 16, the rest of the tile is not used
-  __device__ int cols(int i, int x) const {
-    return min(kKeys, ((x < first ? sinks : hi[i]) - base(x) + 15) & ~15);
-  }
 };
 
 __device__ __forceinline__ Item item_of(const WindowArgs& a, int idx) {
@@ -141,9 +134,12 @@ __device__ __forceinline__ Item item_of(const WindowArgs& a, int idx) {
   it.count = end > 0 ? it.first + (end - it.start + kKeys - 1) / kKeys : 0;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    // (tiles that only the first positions reach into exist only where they run on from 0)
-    it.begin[i] = it.first + (it.lo[i] <= a.sinks ? 0 : (it.lo[i] - it.start) / kKeys);
-    it.last[i] = it.hi[i] > 0 ? it.first + (it.hi[i] - 1 - it.start) / kKeys : -1;
+    it.begin[i] = 0;
+    it.last[i] = -1;  // an empty slot uses no tile
+    if (it.hi[i] == 0) continue;
+    // (where the tiles run on from the first positions, those hold keys for both slots)
+    it.begin[i] = it.first + (it.first == 0 && a.sinks > 0 ? 0 : (it.lo[i] - it.start) / kKeys);
+    it.last[i] = it.first + (it.hi[i] - 1 - it.start) / kKeys;
   }
   return it;
 }
@@ -168,13 +164,12 @@ __device__ __forceinline__ void st_global32(void* p, const uint32_t* v) {
                : "memory");
 }
 
-// Bits [lo, hi) of a 32-bit word (both clamped to it).
+// Bits [lo, hi) of a 32-bit word (clamped to it).
 __device__ __forceinline__ uint32_t bits_between(int lo, int hi) {
-  lo = min(max(lo, 0), 32);
-  hi = min(max(hi, 0), 32);
-  const uint32_t below_hi = hi == 32 ? 0xffffffffu : (1u << hi) - 1u;
-  const uint32_t below_lo = lo == 32 ? 0xffffffffu : (1u << lo) - 1u;
-  return below_hi & ~below_lo;
+  lo = max(lo, 0);
+  uint32_t r;
+  asm("bmsk.clamp.b32 %0, %1, %2;" : "=r"(r) : "r"(lo), "r"(max(hi - lo, 0)));
+  return r;
 }
 
 // Waits (a short time, so without sleep) until a counter in shared memory has reached `need`. A
@@ -234,87 +229,113 @@ struct Shared {
   }
 };
 
+// What the issuing warps need of an item, in registers: the next product has to be ready to go
+// when the buffer it waits for is read.
+struct Turn {
+  int count, first, start, sinks, begin0, begin1, last0, last1, hi0, hi1;
+  __device__ void load(const Item& it) {
+    auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    count = same(it.count);
+    first = same(it.first);
+    start = same(it.start);
+    sinks = same(it.sinks);
+    begin0 = same(it.begin[0]);
+    begin1 = same(it.begin[1]);
+    last0 = same(it.last[0]);
+    last1 = same(it.last[1]);
+    hi0 = same(it.hi[0]);
+    hi1 = same(it.hi[1]);
+  }
+  __device__ bool uses0(int x) const { return x <= last0 && (x < first || x >= begin0); }
+  __device__ bool uses1(int x) const { return x <= last1 && (x < first || x >= begin1); }
+  __device__ int base(int x) const { return x < first ? kKeys * x : start + kKeys * (x - first); }
+  // keys of tile x that slot i multiplies with: a multiple of 16, the rest of the tile is not used
+  __device__ int cols(int i, int x) const {
+    return min(kKeys, ((x < first ? sinks : i ? hi1 : hi0) - base(x) + 15) & ~15);
+  }
+};
+
 // S = Q K^T for slot 0 and slot 1 in turn, tile by tile, each as soon as its buffer has been read.
 // A whole warp walks the tiles in step; one of its lanes issues.
 template <int HD>
-__device__ __forceinline__ void issue_scores(const Shared<HD>& sm, const WaitGuard& guard, uint32_t tmem) {
+__device__ __forceinline__ bool issue_scores(const Shared<HD>& sm, const WaitGuard& guard, uint32_t tmem) {
   using L = Layout<HD>;
   constexpr uint32_t IDESC_S = idesc_bf16(128, 0, false, false);  // + columns / 8 << 17
   const uint32_t one = elect_one();
   const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(sm.q)), k_desc = sdesc_kmajor_sw128(smem_u32(sm.k));
-  uint32_t stage = 0, par = 0, n0 = 0, n1 = 0;  // K stage and its parity, S products of each slot so far
-  bool ok = true;
-  for (int k = 0; ok; ++k) {
-    if (!(ok = mbar_sleep_warp(&sm.item_full[k % kItems], (k / kItems) & 1, guard))) break;
-    const Item& it = sm.items[k % kItems];
-    const int count = __shfl_sync(0xffffffffu, it.count, 0);
-    if (count == 0) break;
-    for (int x = 0; ok && x < count; ++x) {
-      if (!(ok = mbar_sleep_warp(&sm.k_full[stage], par, guard))) break;
-      const bool both = __shfl_sync(0xffffffffu, it.uses(0, x) && it.uses(1, x), 0);
-      const int from = __shfl_sync(0xffffffffu, it.uses(0, x) ? 0 : 1, 0), to = both ? 2 : from + 1;
+  uint32_t stage = 0, par = 0, n0 = 0, n1 = 0, q0 = 0, q1 = 0;  // K stage and its parity, S products and items of each slot
+  Turn t;
+  for (int k = 0;; ++k) {
+    if (!mbar_sleep_warp(&sm.item_full[k % kItems], (k / kItems) & 1, guard)) return false;
+    t.load(sm.items[k % kItems]);
+    __syncwarp();
+    if (one) mbar_arrive(&sm.item_empty[k % kItems]);
+    if (t.count == 0) return true;
+    bool begun0 = false, begun1 = false;
+    for (int x = 0; x < t.count; ++x) {
+      const bool u0 = t.uses0(x), u1 = t.uses1(x);
+      const uint64_t kd = k_desc + stage * (L::kKB / 16);
+      if (!mbar_sleep_warp(&sm.k_full[stage], par, guard)) return false;
 #pragma unroll 1
-      for (int i = from; i < to; ++i) {
-        const int cols = __shfl_sync(0xffffffffu, it.cols(i, x), 0);
+      for (int i = u0 ? 0 : 1; i < (u1 ? 2 : 1); ++i) {
+        const uint32_t idesc = IDESC_S | (static_cast<uint32_t>(t.cols(i, x)) >> 3 << 17), d = tmem + L::col_s(i);
+        const uint64_t qd = q_desc + i * (L::kQB / 16);
         const uint32_t mine = i ? n1 : n0, before = L::kSharedS ? n0 + n1 : mine;
-        // (the slot's k-th item has its queries in the k-th filling that it took part in)
-        if (x == __shfl_sync(0xffffffffu, it.first_used(i), 0) &&
-            !(ok = mbar_sleep_warp(&sm.q_full[i], __shfl_sync(0xffffffffu, it.nth[i], 0) & 1, guard)))
-          break;
+        if (!(i ? begun1 : begun0) && !mbar_sleep_warp(&sm.q_full[i], (i ? q1 : q0) & 1, guard)) return false;
         // the scores before it have been read out of the buffer
-        if (before > 0 && !(ok = mbar_sleep_warp(&sm.s_free[L::kSharedS ? 0 : i], (before - 1) & 1, guard))) break;
-        if (i)
-          ++n1;
-        else
-          ++n0;
+        if (before > 0 && !mbar_sleep_warp(&sm.s_free[L::kSharedS ? 0 : i], (before - 1) & 1, guard)) return false;
         tc_fence_after();
-        const uint64_t qd = q_desc + i * (L::kQB / 16), kd = k_desc + stage * (L::kKB / 16);
-        const uint32_t idesc = IDESC_S | (static_cast<uint32_t>(cols) >> 3 << 17), d = tmem + L::col_s(i);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
           umma_ss_one(one, d, qd + (kk >> 2) * (L::kBox / 16) + (kk & 3) * 2,
                       kd + (kk >> 2) * (L::kBox / 16) + (kk & 3) * 2, idesc, kk > 0);
         umma_commit_one(one, &sm.s_full[i]);
         if (one) sm.s_issued[i] = mine + 1;
-        if (i + 1 == to) umma_commit_one(one, &sm.k_empty[stage]);
-        if (x == __shfl_sync(0xffffffffu, it.last[i], 0)) umma_commit_one(one, &sm.q_empty[i]);
+        if (i == 1 || !u1) umma_commit_one(one, &sm.k_empty[stage]);
+        if (x == (i ? t.last1 : t.last0)) umma_commit_one(one, &sm.q_empty[i]);
+        if (i) {
+          ++n1;
+          q1 += !begun1;
+          begun1 = true;
+        } else {
+          ++n0;
+          q0 += !begun0;
+          begun0 = true;
+        }
       }
       if (++stage == L::kStagesK) {
         stage = 0;
         par ^= 1;
       }
     }
-    __syncwarp();
-    if (one) mbar_arrive(&sm.item_empty[k % kItems]);
   }
-  if (!ok) give_up(guard);
-  if (*guard.abort) {
-    umma_commit_one(one, &sm.drains[0]);
-    if (one) drain_wait(&sm.drains[0], 0);
-  }
-  __syncwarp();
 }
 
 // O += P V in the same order, by a warp of its own (its lanes clear the rows of V past a clip's
 // end). The tensor core runs products in the order they are issued: a slot's next S, which its
 // softmax waits for, goes ahead of its P V.
 template <int HD>
-__device__ __forceinline__ void issue_outputs(const WindowArgs& args, const Shared<HD>& sm, const WaitGuard& guard,
+__device__ __forceinline__ bool issue_outputs(const WindowArgs& args, const Shared<HD>& sm, const WaitGuard& guard,
                                               uint32_t tmem) {
   using L = Layout<HD>;
   constexpr uint32_t IDESC_O = idesc_bf16(128, HD, false, true);
   const uint32_t lane = threadIdx.x & 31, one = elect_one();
   const uint64_t v_desc = sdesc_mnmajor_sw128(smem_u32(sm.v), L::kBox);
   uint32_t stage = 0, par = 0, n0 = 0, n1 = 0;  // V stage and its parity, P V products of each slot so far
-  bool ok = true;
-  for (int k = 0; ok; ++k) {
-    if (!(ok = mbar_sleep_warp(&sm.item_full[k % kItems], (k / kItems) & 1, guard))) break;
-    const Item& it = sm.items[k % kItems];
-    const int count = __shfl_sync(0xffffffffu, it.count, 0);
-    if (count == 0) break;
-    for (int x = 0; ok && x < count; ++x) {
-      if (!(ok = mbar_sleep_warp(&sm.v_full[stage], par, guard))) break;
-      const int clear = __shfl_sync(0xffffffffu, it.n < args.T ? it.n - it.base(x) : kKeys, 0);
+  Turn t;
+  for (int k = 0;; ++k) {
+    if (!mbar_sleep_warp(&sm.item_full[k % kItems], (k / kItems) & 1, guard)) return false;
+    t.load(sm.items[k % kItems]);
+    const int n = __shfl_sync(0xffffffffu, sm.items[k % kItems].n, 0);
+    __syncwarp();
+    if (one) mbar_arrive(&sm.item_empty[k % kItems]);
+    if (t.count == 0) return true;
+    bool begun0 = false, begun1 = false;
+    for (int x = 0; x < t.count; ++x) {
+      const bool u0 = t.uses0(x), u1 = t.uses1(x);
+      const int clear = n < args.T ? n - t.base(x) : kKeys;
+      const uint64_t vd = v_desc + stage * (L::kKB / 16);
+      if (!mbar_sleep_warp(&sm.v_full[stage], par, guard)) return false;
       if (clear < kKeys) {
         // rows past the clip's length hold anything (NaN times a weight of zero is NaN): zeros
         for (int r = clear + (lane >> 3); r < kKeys; r += 4)
@@ -324,40 +345,43 @@ __device__ __forceinline__ void issue_outputs(const WindowArgs& args, const Shar
         fence_proxy_async_smem();
         __syncwarp();
       }
-      const bool both = __shfl_sync(0xffffffffu, it.uses(0, x) && it.uses(1, x), 0);
-      const int from = __shfl_sync(0xffffffffu, it.uses(0, x) ? 0 : 1, 0), to = both ? 2 : from + 1;
 #pragma unroll 1
-      for (int i = from; i < to; ++i) {
-        const int cols = __shfl_sync(0xffffffffu, it.cols(i, x), 0);
-        const bool adds = __shfl_sync(0xffffffffu, x != it.first_used(i), 0);
-        const uint32_t mine = i ? n1 : n0;
-        if (!(ok = mbar_sleep_warp(&sm.p_full[i], mine & 1, guard))) break;
-        if (x != __shfl_sync(0xffffffffu, it.last[i], 0) && !(ok = wait_count(&sm.s_issued[i], mine + 2, guard))) break;
-        if (i)
-          ++n1;
-        else
-          ++n0;
+      for (int i = u0 ? 0 : 1; i < (u1 ? 2 : 1); ++i) {
+        const int cols = t.cols(i, x);
+        const uint32_t mine = i ? n1 : n0, d = tmem + L::col_o(i), pa = tmem + L::col_p(i);
+        const bool adds = i ? begun1 : begun0;
+        if (!mbar_sleep_warp(&sm.p_full[i], mine & 1, guard)) return false;
+        if (x != (i ? t.last1 : t.last0) && !wait_count(&sm.s_issued[i], mine + 2, guard)) return false;
         tc_fence_after();
-        const uint64_t vd = v_desc + stage * (L::kKB / 16);
-        const uint32_t d = tmem + L::col_o(i), pa = tmem + L::col_p(i);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
           if (kk * 16 < cols) umma_ts_one(one, d, pa + kk * 8, vd + kk * (2048 / 16), IDESC_O, (adds || kk > 0));
         umma_commit_one(one, &sm.pv_done[i]);
-        if (i + 1 == to) umma_commit_one(one, &sm.v_empty[stage]);
+        if (i == 1 || !u1) umma_commit_one(one, &sm.v_empty[stage]);
+        if (i) {
+          ++n1;
+          begun1 = true;
+        } else {
+          ++n0;
+          begun0 = true;
+        }
       }
       if (++stage == L::kStagesV) {
         stage = 0;
         par ^= 1;
       }
     }
-    __syncwarp();
-    if (one) mbar_arrive(&sm.item_empty[k % kItems]);
   }
+}
+
+// Behind an issuing warp whose wait gave up, or whose block is winding down: its products still in
+// flight complete before the block's tensor memory goes.
+__device__ __forceinline__ void drain_products(uint64_t* bar, bool ok, const WaitGuard& guard) {
   if (!ok) give_up(guard);
   if (*guard.abort) {
-    umma_commit_one(one, &sm.drains[1]);
-    if (one) drain_wait(&sm.drains[1], 0);
+    const uint32_t one = elect_one();
+    umma_commit_one(one, bar);
+    if (one) drain_wait(bar, 0);
   }
   __syncwarp();
 }
@@ -434,71 +458,70 @@ __global__ void __launch_bounds__(kThreads, 1)
     setmaxnreg_dec<kRegsCtrl>();
   if (warp == 0) {
     if (lane == 0) {
+      // keys, and behind an item's first tile its queries, as soon as the last S before has read its slot's
       for (int k = 0; ok; ++k) {
         if (!(ok = item_ready(k))) break;
         const Item& it = items[k % kItems];
         if (it.count == 0) break;
         for (int x = 0; ok && x < it.count; ++x) {
-          const uint32_t sk = loads_k % NK, sv = loads_v % NV;
-          const int row = it.base(x);
-          if (!(ok = mbar_sleep(&k_empty[sk], ((loads_k / NK) & 1) ^ 1, guard))) break;
-          mbar_arrive_expect_tx(&k_full[sk], L::kKB);
+          const uint32_t s = loads_k % NK;
+          if (!(ok = mbar_sleep(&k_empty[s], ((loads_k / NK) & 1) ^ 1, guard))) break;
+          mbar_arrive_expect_tx(&k_full[s], L::kKB);
           for (int b = 0; b < L::kBoxes; ++b)
-            tma_load_3d(sK + sk * L::kKB + b * L::kBox, &tmK, &k_full[sk], 64 * b, row, it.kv);
+            tma_load_3d(sK + s * L::kKB + b * L::kBox, &tmK, &k_full[s], 64 * b, it.base(x), it.kv);
           ++loads_k;
-          if (!(ok = mbar_sleep(&v_empty[sv], ((loads_v / NV) & 1) ^ 1, guard))) break;
-          mbar_arrive_expect_tx(&v_full[sv], L::kKB);
-          for (int b = 0; b < L::kBoxes; ++b)
-            tma_load_3d(sV + sv * L::kKB + b * L::kBox, &tmV, &v_full[sv], 64 * b, row, it.kv);
-          ++loads_v;
+          for (int i = 0; x == 0 && ok && i < 2; ++i) {
+            if (it.hi[i] == 0) continue;
+            if (!(ok = mbar_sleep(&q_empty[i], (it.nth[i] & 1) ^ 1, guard))) break;
+            mbar_arrive_expect_tx(&q_full[i], L::kQB);
+            for (int b = 0; b < L::kBoxes; ++b)
+              tma_load_3d(sQ + i * L::kQB + b * L::kBox, &tmQ, &q_full[i], 64 * b, it.row[i],
+                          it.b * args.heads + it.head[i]);
+            loads_q[i] = it.nth[i] + 1;
+          }
         }
         done_with(k);
       }
     }
   } else if (warp == 1) {
-    issue_scores<HD>(sm, guard, tmem);
+    drain_products(&sm.drains[0], issue_scores<HD>(sm, guard, tmem), guard);
   } else if (warp == 2) {
-    issue_outputs<HD>(args, sm, guard, tmem);
+    drain_products(&sm.drains[1], issue_outputs<HD>(args, sm, guard, tmem), guard);
   } else if (warp == 3) {
     if (lane == 0) {
       // works the items out one ahead of the other roles (those past a clip's end are left out, an
-      // item of no tiles is the end), and loads their queries as soon as a slot's last S has read
-      // the ones before
-      int idx = blockIdx.x;
-      int nth[2] = {0, 0};
-      auto publish = [&](int k) {
-        Item it;
-        it.count = 0;
+      // item of no tiles is the end), and loads the values: a thread of its own, so that a key tile
+      // never waits for a value tile's place
+      int idx = blockIdx.x, nth[2] = {0, 0};
+      Item now, next;
+      for (int k = -1; ok; ++k) {
+        next.count = 0;
         for (; idx < args.items; idx += gridDim.x) {
-          it = item_of(args, idx);
-          if (it.count > 0) break;
+          next = item_of(args, idx);
+          if (next.count > 0) break;
         }
         idx += gridDim.x;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          it.nth[i] = nth[i];
-          nth[i] += it.count > 0 && it.hi[i] > 0;
+          next.nth[i] = nth[i];
+          nth[i] += next.count > 0 && next.hi[i] > 0;
         }
-        if ((ok = mbar_sleep(&item_empty[k % kItems], ((k / kItems) & 1) ^ 1, guard))) {
-          items[k % kItems] = it;
-          mbar_arrive(&item_full[k % kItems]);
-        }
-        return it;
-      };
-      Item now = publish(0);
-      for (int k = 0; ok && now.count > 0; ++k) {
-        const Item next = publish(k + 1);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (!ok || now.hi[i] == 0) continue;
-          if (!(ok = mbar_sleep(&q_empty[i], (loads_q[i] & 1) ^ 1, guard))) continue;
-          mbar_arrive_expect_tx(&q_full[i], L::kQB);
-          for (int b = 0; b < L::kBoxes; ++b)
-            tma_load_3d(sQ + i * L::kQB + b * L::kBox, &tmQ, &q_full[i], 64 * b, now.row[i],
-                        now.b * args.heads + now.head[i]);
-          ++loads_q[i];
+        const int at = (k + 1) % kItems;
+        if (!(ok = mbar_sleep(&item_empty[at], (((k + 1) / kItems) & 1) ^ 1, guard))) break;
+        items[at] = next;
+        mbar_arrive(&item_full[at]);
+        if (k >= 0) {
+          for (int x = 0; ok && x < now.count; ++x) {
+            const uint32_t s = loads_v % NV;
+            if (!(ok = mbar_sleep(&v_empty[s], ((loads_v / NV) & 1) ^ 1, guard))) break;
+            mbar_arrive_expect_tx(&v_full[s], L::kKB);
+            for (int b = 0; b < L::kBoxes; ++b)
+              tma_load_3d(sV + s * L::kKB + b * L::kBox, &tmV, &v_full[s], 64 * b, now.base(x), now.kv);
+            ++loads_v;
+          }
         }
         now = next;
+        if (now.count == 0) break;
       }
     }
   }
@@ -519,30 +542,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int key_lo = max(0, p - args.left), key_hi = min(it.n, p + args.right + 1);
       float m_ref = -INFINITY, l = 0.f;
       bool begun = false;
-      const int last = it.last[slot], first = it.first;
-      for (int x = it.first_used(slot); x <= last; x = it.next_used(slot, x)) {
+      const int first = it.first, begin = it.begin[slot], last = it.last[slot], start = it.start;
+      for (int x = first > 0 ? 0 : begin; x <= last; x = x + 1 == first ? begin : x + 1) {
         if (!(ok = mbar_sleep_warp(&s_full[slot], n_s & 1, guard))) break;
         tc_fence_after();
         uint32_t r[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld32(colS + 32 * c, r[c]);
-        const int base = it.base(x);
-        const int c_lo = x < first ? 0 : key_lo - base, c_hi = x < first ? 0 : key_hi - base;
+        const int base = x < first ? kKeys * x : start + kKeys * (x - first);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_free[L::kSharedS ? 0 : slot]);  // back to the tensor core
+        // P V of the tile before must be complete before O is rescaled or P overwritten (asked for here,
+        // needed below)
+        const bool pv_ok = n_s == 0 || mbar_test(&pv_done[slot], (n_s - 1) & 1);
         // 32-column chunks that some row of the warp sees (the others cost nothing below)
         uint32_t live = 15u;
-        if (!__all_sync(0xffffffffu, c_hi >= kKeys && c_lo <= 0)) {
-          const int c_sink = min(args.sinks, key_hi) - base;
+        if (__any_sync(0xffffffffu, x < first || base < key_lo || base + kKeys > key_hi)) {
+          // a tile of first positions ends at the last of them; where the tiles run on from position 0
+          // the first positions add to the window's
+          const bool early = x < first;
+          const int extra = early || first > 0 ? 0 : args.sinks;
           live = 0;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const uint32_t seen = bits_between(c_lo - 32 * c, c_hi - 32 * c) | bits_between(0, c_sink - 32 * c);
+            const int at = base + 32 * c;
+            const uint32_t seen = early ? bits_between(0, args.sinks - at)
+                                        : bits_between(key_lo - at, key_hi - at) | bits_between(0, min(extra, key_hi) - at);
             if (__any_sync(0xffffffffu, seen != 0)) {
               live |= 1u << c;
-              if (!__all_sync(0xffffffffu, seen == 0xffffffffu)) {
+              if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                   if (!((seen >> i) & 1u)) r[c][i] = 0xff800000u;  // -inf
@@ -584,11 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 16; ++i) r[c >> 1][(c & 1) * 16 + i] = 0;
           }
         }
-        if (n_s > 0) {
-          // P V of the tile before must be complete before O is rescaled or P overwritten
-          if (!(ok = mbar_sleep_warp(&pv_done[slot], (n_s - 1) & 1, guard))) break;
-          tc_fence_after();
-        }
+        if (!__all_sync(0xffffffffu, pv_ok) && !(ok = mbar_sleep_warp(&pv_done[slot], (n_s - 1) & 1, guard))) break;
+        tc_fence_after();
         tmem_st32(colP, r[0]);
         tmem_st32(colP + 32, r[1]);
         if (begun && __any_sync(0xffffffffu, rescale)) {
@@ -622,22 +649,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const float inv_l = 1.0f / l;
 #pragma unroll 1
-      for (int c = 0; c < HD / 32; ++c) {
-        uint32_t u[32];
-        tmem_ld32(colO + 32 * c, u);
+      for (int c = 0; c < HD / 64; ++c) {
+        uint32_t u[2][32];
+        tmem_ld32(colO + 64 * c, u[0]);
+        tmem_ld32(colO + 64 * c + 32, u[1]);
         tmem_wait_ld();
         if (stored) {
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            u[i] = pack_bf16x2(__uint_as_float(u[2 * i]) * inv_l, __uint_as_float(u[2 * i + 1]) * inv_l);
+          for (int i = 0; i < 32; ++i)
+            u[0][i] = pack_bf16x2(__uint_as_float(u[i >> 4][2 * (i & 15)]) * inv_l,
+                                  __uint_as_float(u[i >> 4][2 * (i & 15) + 1]) * inv_l);
           if (args.wide) {  // a whole 32-byte sector at a time
 #pragma unroll
-            for (int i = 0; i < 2; ++i) st_global32(SAL_CK_ST(dst + 32 * c + 16 * i, 32), &u[8 * i]);
+            for (int i = 0; i < 4; ++i) st_global32(SAL_CK_ST(dst + 64 * c + 16 * i, 32), &u[0][8 * i]);
           } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *SAL_CK_ST(reinterpret_cast<uint4*>(dst + 32 * c) + i, 16) =
-                  make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+            for (int i = 0; i < 8; ++i)
+              *SAL_CK_ST(reinterpret_cast<uint4*>(dst + 64 * c) + i, 16) =
+                  make_uint4(u[0][4 * i], u[0][4 * i + 1], u[0][4 * i + 2], u[0][4 * i + 3]);
           }
         }
       }
