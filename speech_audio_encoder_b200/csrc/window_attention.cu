@@ -313,7 +313,7 @@ __device__ __forceinline__ bool issue_scores(const Shared<HD>& sm, const WaitGua
 
 // O += P V in the same order, by a warp of its own (its lanes clear the rows of V past a clip's
 // end). The tensor core runs products in the order they are issued: a slot's next S, which its
-// softmax waits for, goes ahead of its P V.
+// softmax waits for, goes ahead of its P V (unless it is not among the very next ones).
 template <int HD>
 __device__ __forceinline__ bool issue_outputs(const WindowArgs& args, const Shared<HD>& sm, const WaitGuard& guard,
                                               uint32_t tmem) {
@@ -351,7 +351,7 @@ __device__ __forceinline__ bool issue_outputs(const WindowArgs& args, const Shar
         const uint32_t mine = i ? n1 : n0, d = tmem + L::col_o(i), pa = tmem + L::col_p(i);
         const bool adds = i ? begun1 : begun0;
         if (!mbar_sleep_warp(&sm.p_full[i], mine & 1, guard)) return false;
-        if (x != (i ? t.last1 : t.last0) && !wait_count(&sm.s_issued[i], mine + 2, guard)) return false;
+        if ((i ? t.uses1(x + 1) : t.uses0(x + 1)) && !wait_count(&sm.s_issued[i], mine + 2, guard)) return false;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
