@@ -574,7 +574,8 @@ sal_status sal_cache_compact(const sal_cache* cache, int32_t* table_out, int32_t
  * row b at q + b * q_row_stride + h * q_head_stride (elements; multiples of 8), bf16; o
  * [batch, heads * head_dim] bf16. window may be NULL; its `right` is not used. A row with
  * nothing visible (length 0, a sequence out of range, every page let go) gives zeros.
- * workspace: sal_attention_paged_workspace_bytes() bytes, 256-byte aligned; calls that may
+ * workspace: sal_attention_paged_workspace_bytes() bytes, 256-byte aligned, zero-filled by
+ * the caller before its first use (every call leaves it ready for the next); calls that may
  * overlap on the GPU need workspaces of their own. Errors: SAL_EINVAL, SAL_ESHAPE (batch
  * or heads > 65,535), SAL_EWORKSPACE, SAL_EDEVICE, SAL_ECUDA. */
 size_t sal_attention_paged_workspace_bytes(const sal_cache* cache, int batch, int heads);

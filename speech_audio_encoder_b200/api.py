@@ -760,8 +760,9 @@ def sal_cache_compact(cache: PagedCache, out: PagedCache | None = None, stream=N
 
 
 def attention_paged_workspace(cache: PagedCache, batch: int, heads: int) -> torch.Tensor:
+    """Scratch of sal_attention_paged (zero-filled, as its first use needs it)."""
     n = lib().sal_attention_paged_workspace_bytes(cache.ref, batch, heads)
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=cache.k.device)
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=cache.k.device)
 
 
 def sal_attention_paged(q: torch.Tensor, cache: PagedCache, left: int = -1, sinks: int = 0, layer: int = 0,

@@ -58,6 +58,8 @@ struct PagedArgs {
   // among all (row, group) pairs, or by its first part where there are fewer of those
   int4* joins;
   int by_part;
+  int* arrived;  // [grid] pieces that are there of what begins in a part: zero between calls
+  int inside;    // the last piece's block joins them; else paged_join_kernel does
   int64_t q_row, q_head;
   const int32_t *table, *lengths, *seqs;
   int batch, heads, kv_heads, row_tiles, pages, page_shift, sequences, max_pages;
@@ -335,13 +337,15 @@ __global__ void __launch_bounds__(kThreads, 2) paged_cluster_kernel(const PagedA
 // Many keys: the blocks of keys of all rows and key heads in one line, cut into equal parts,
 // one for each block that fits on the GPU, so that rows of any lengths keep every SM busy to
 // the end. A part may end one row's keys and begin another's: what lies wholly inside a part is
-// written out, the at most two pieces that do not go to the workspace, and paged_join_kernel
-// puts them together. The lengths are on the device, so every block adds them up for itself.
+// written out, the at most two pieces that do not go to the workspace, and the block that brings
+// the last piece of a row, or paged_join_kernel, puts them together in their order, so the
+// result does not depend on which came last. The lengths are on the device, so every block adds them up for itself.
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 2) paged_line_kernel(const PagedArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t sums[kWarps];
   __shared__ int64_t found[2];  // where the part's first row begins, and which row it is
+  __shared__ int last_here;
   const int tid = threadIdx.x, groups = a.kv_heads * a.row_tiles, share = a.heads / a.kv_heads;
   pdl_wait();
   pdl_trigger();
@@ -401,16 +405,20 @@ __global__ void __launch_bounds__(kThreads, 2) paged_line_kernel(const PagedArgs
       const int rows = min(kRowTile, share - r0), h0 = kvh * share + r0;
       walk<HD>(a, sp, seq, b, kvh, h0, rows, lo, hi, smem);
       const bool whole = lo == 0 && hi == sp.blocks;
-      int4 cut = make_int4(b, group, c, 0);
-      if (lo == 0 && !whole) {  // begins here and ends in the part that holds its last block
-        const int64_t last = begin + sp.blocks - 1;
-        int64_t e = last * parts / units;  // the part with units * e / parts <= last < units * (e + 1) / parts
-        while (units * (e + 1) / parts <= last) ++e;
-        while (units * e / parts > last) --e;
-        cut.w = static_cast<int>(e) - c + 1;
-        join = cut;
+      // the part that holds unit v: units * e / parts <= v < units * (e + 1) / parts
+      auto part_of = [&](int64_t v) {
+        int64_t e = v * parts / units;
+        while (units * (e + 1) / parts <= v) ++e;
+        while (units * e / parts > v) --e;
+        return static_cast<int>(e);
+      };
+      const int from = whole || lo == 0 ? c : part_of(begin);
+      const int pieces = whole ? 0 : part_of(begin + sp.blocks - 1) - from + 1;
+      if (lo == 0 && !a.inside) {
+        const int4 cut = make_int4(b, group, c, pieces);
+        if (!whole) join = cut;
+        if (tid == 0 && !a.by_part) *SAL_CK_ST(a.joins + b * groups + group, 16) = cut;
       }
-      if (lo == 0 && tid == 0 && !a.by_part) *SAL_CK_ST(a.joins + b * groups + group, 16) = cut;
       const int d = tid % HD;
       for (int r = tid / HD; r < rows; r += kThreads / HD) {
         float x, mm, total;
@@ -423,16 +431,40 @@ __global__ void __launch_bounds__(kThreads, 2) paged_line_kernel(const PagedArgs
         *SAL_CK_ST(a.part + to * HD + d, 4) = x;
         if (d == 0) *SAL_CK_ST(a.stats + to, 8) = make_float2(mm, total);
       }
+      if (!whole && a.inside) {
+        // whichever block brings the last piece joins them all, in their order
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) last_here = atomicAdd(SAL_CK_ST(a.arrived + from, 4), 1) == pieces - 1;
+        __syncthreads();
+        if (last_here) {
+          __threadfence();
+          for (int r = tid / HD; r < rows; r += kThreads / HD) {
+            float mm = -INFINITY, x = 0.f, total = 0.f;
+            auto place = [&](int w) { return (2 * (from + w) + (w == 0)) * kRowTile + r; };
+            for (int w = 0; w < pieces; ++w) mm = fmaxf(mm, __ldcg(SAL_CK_LD(a.stats + place(w), 8)).x);
+#pragma unroll 4
+            for (int w = 0; w < pieces; ++w) {
+              const float2 st = __ldcg(SAL_CK_LD(a.stats + place(w), 8));
+              const float f = st.y > 0.f ? fast_exp2(st.x - mm) : 0.f;
+              total += st.y * f;
+              x += __ldcg(SAL_CK_LD(a.part + place(w) * HD + d, 4)) * f;
+            }
+            store_out<HD>(a, b, h0 + r, d, x, total);
+          }
+          if (tid == 0) *SAL_CK_ST(a.arrived + from, 4) = 0;
+        }
+      }
       u = begin + hi;
       __syncthreads();  // the merge has read what the next walk's copies overwrite
     }
   }
-  if (tid == 0 && a.by_part) *SAL_CK_ST(a.joins + c, 16) = join;
+  if (tid == 0 && a.by_part && !a.inside) *SAL_CK_ST(a.joins + c, 16) = join;
   // rows without keys have no part: zeros
   for (int b = c; b < a.batch; b += gridDim.x)
     if (span_of(a, seq_of(b)).blocks == 0) {
       for (int i = tid; i < a.heads * HD; i += kThreads) store_out<HD>(a, b, 0, i, 0.f, 0.f);
-      if (!a.by_part)
+      if (!a.by_part && !a.inside)
         for (int i = tid; i < groups; i += kThreads) *SAL_CK_ST(a.joins + b * groups + i, 16) = make_int4(0, 0, 0, 0);
     }
 }
@@ -529,9 +561,10 @@ Plan plan_of(const sal_cache* c, int batch, int heads, int64_t keys) {
 }
 
 constexpr size_t kJoinBytes = (kSlots * sizeof(int4) + 255) & ~size_t(255);
+constexpr size_t kArrivedBytes = (kSlots * sizeof(int) + 255) & ~size_t(255);
 constexpr size_t kStatBytes = kSlots * 2 * kRowTile * sizeof(float2);
 size_t workspace_bytes(int head_dim) {
-  return kJoinBytes + kStatBytes + static_cast<size_t>(kSlots) * 2 * kRowTile * head_dim * 4;
+  return kArrivedBytes + kJoinBytes + kStatBytes + static_cast<size_t>(kSlots) * 2 * kRowTile * head_dim * 4;
 }
 
 std::mutex g_mu;
@@ -567,6 +600,7 @@ sal_status launch(const PagedArgs& a, const Plan& p, cudaStream_t s, const std::
   const unsigned grid = static_cast<unsigned>(p.grid);
   if (launch_kernel(paged_line_kernel<HD>, dim3(grid), dim3(kThreads), Ring<HD>::kBytes, s, a) != cudaSuccess)
     return SAL_ECUDA;
+  if (a.inside) return SAL_OK;
   const int rows = std::min(kRowTile, a.heads / a.kv_heads);
   declare();
   const unsigned entries = a.by_part ? grid : static_cast<unsigned>(a.batch) * groups;
@@ -635,9 +669,15 @@ sal_status sal_attention_paged(const void* q, int64_t q_row_stride, int64_t q_he
   a.splits = plan.splits;
   a.by_part = static_cast<int64_t>(batch) * cache->kv_heads * plan.row_tiles > plan.grid;
   a.batch = batch;
-  a.joins = static_cast<int4*>(workspace);
-  a.stats = reinterpret_cast<float2*>(static_cast<char*>(workspace) + kJoinBytes);
-  a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + kJoinBytes + kStatBytes);
+  char* w = static_cast<char*>(workspace);
+  a.arrived = reinterpret_cast<int*>(w);
+  a.joins = reinterpret_cast<int4*>(w + kArrivedBytes);
+  a.stats = reinterpret_cast<float2*>(w + kArrivedBytes + kJoinBytes);
+  a.part = reinterpret_cast<float*>(w + kArrivedBytes + kJoinBytes + kStatBytes);
+  // One thread owns a column of a row and reads its pieces one after the other: worth it for few of
+  // both (the second launch costs 4 us more); many rows or pieces go to a kernel with a block per row.
+  const int64_t pairs = static_cast<int64_t>(batch) * cache->kv_heads * plan.row_tiles;
+  a.inside = heads / cache->kv_heads <= 4 && pairs >= 32;
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(hd));
   const auto declare = [&] {
     ck_declare(q, ((batch - 1) * q_row_stride + (heads - 1) * q_head_stride + hd) * 2, false);
