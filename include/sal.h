@@ -279,8 +279,8 @@ int sal_checked_build(void);
 /* Synchronises the current device and reports, then clears, the accesses the checked
  * build refused on it since the last report: their count, the lowest address, the source
  * file of that access (1 frontend.cu, 2 rowops.cu, 3 gemm.cu, 4 attention.cu, 5 ctc.cu,
- * 6 window_attention.cu, 7 paged_attention.cu, 8 cache.cu) and line, and the smallest
- * sal_launch_count value before a launch that made one. All outputs are 0 when count is 0.
+ * 6 window_attention.cu, 7 paged_attention.cu, 8 cache.cu, 9 stream.cu) and line, and the
+ * smallest sal_launch_count value before a launch that made one. All outputs are 0 when count is 0.
  * SAL_EINVAL (outputs 0) from libsal.so or on a null pointer; SAL_ECUDA if the device
  * cannot be reached. */
 sal_status sal_check_report(uint64_t* count, uint64_t* first_address, int* file, int* line,
@@ -521,8 +521,8 @@ typedef struct {
 size_t sal_cache_workspace_bytes(int pages, int sequences);
 
 /* Writes new keys and values into a layer's pages: token t of row b, k and v [batch,
- * kv_heads, T, head_dim] bf16, goes to position starts[b] + t of sequence seqs[b] (NULL:
- * b). Tokens at positions outside [0, lengths[seq]), or whose page has been let go, and
+ * kv_heads, T, head_dim] bf16, goes to position starts[b] + t (starts NULL: t) of sequence
+ * seqs[b] (NULL: b). Tokens at positions outside [0, lengths[seq]), or whose page has been let go, and
  * rows with a sequence out of range, are skipped: so a row may bring fewer than T tokens,
  * and one whose sal_cache_resize failed writes nothing. Two tokens for one position (a
  * sequence named twice, or a page that two rows share) leave one of them there. */
@@ -582,6 +582,32 @@ size_t sal_attention_paged_workspace_bytes(const sal_cache* cache, int batch, in
 sal_status sal_attention_paged(const void* q, int64_t q_row_stride, int64_t q_head_stride, int batch, int heads,
                                const sal_cache* cache, int layer, const int32_t* seqs, const sal_window* window,
                                void* o, void* workspace, size_t ws_bytes, void* stream);
+
+/* The encoder's layers over live streams, causal: position p of a stream sees itself, the
+ * window->left positions before it (< 0: all) and the first window->sinks (window may be NULL:
+ * everything before it; `right` is not used). Keys and values of every layer are kept in the
+ * cache (kv_heads 10, head_dim 128, at least n_layers layers; layer i of w uses layer i).
+ *
+ * sal_stream_prefill takes `batch` streams from their start: x [batch, T, 1280] float32 holds
+ * x0 of positions 0 .. lengths[b] - 1 (lengths int32 [batch], NULL: all T; rows past a length are
+ * computed from what they hold and mean nothing) and, after the call, the residual stream; emb
+ * [batch, T, 1280] bf16 the final LayerNorm of it. The keys and values go to sequence seqs[b]
+ * (NULL: b), which sal_cache_resize must have given the length lengths[b] before; what the
+ * window has already let go is not kept.
+ * sal_stream_step takes one new position of each row's stream: x [batch, 1280] float32 is x0 of
+ * position p = lengths[seq] - 1 of the cache, which sal_cache_resize must have made longer by one
+ * before; emb [batch, 1280] bf16. A sequence may be named once. A row whose sequence is out of
+ * range or empty, or whose page has been let go, keeps no key and value; its emb is that of a
+ * position that sees what the cache has left of its keys.
+ * Both clobber x. workspace: 256-byte aligned, sal_stream_workspace_bytes(batch, T) bytes (T = 1
+ * for a step). Errors: as sal_encoder_forward, and as the cache calls. */
+size_t sal_stream_workspace_bytes(int batch, int64_t T);
+sal_status sal_stream_prefill(float* x, int batch, int64_t T, const int32_t* lengths, const sal_weights* w,
+                              int n_layers, const sal_window* window, const sal_cache* cache, const int32_t* seqs,
+                              void* emb, void* workspace, size_t ws_bytes, void* stream);
+sal_status sal_stream_step(float* x, int batch, const sal_weights* w, int n_layers, const sal_window* window,
+                           const sal_cache* cache, const int32_t* seqs, void* emb, void* workspace, size_t ws_bytes,
+                           void* stream);
 
 #ifdef __cplusplus
 }

@@ -173,6 +173,14 @@ EXPORTS = {
                                             ctypes.c_int, ctypes.POINTER(sal_cache), ctypes.c_int, ctypes.c_void_p,
                                             ctypes.POINTER(sal_window), ctypes.c_void_p, ctypes.c_void_p,
                                             ctypes.c_size_t, ctypes.c_void_p]),
+    "sal_stream_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int64]),
+    "sal_stream_prefill": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_void_p,
+                                           ctypes.POINTER(sal_weights), ctypes.c_int, ctypes.POINTER(sal_window),
+                                           ctypes.POINTER(sal_cache), ctypes.c_void_p, ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "sal_stream_step": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.POINTER(sal_weights), ctypes.c_int,
+                                        ctypes.POINTER(sal_window), ctypes.POINTER(sal_cache), ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
 }
 
 _libs: dict = {}
@@ -543,7 +551,7 @@ def sal_set_wait_limit_ns(ns: int) -> None:
 
 
 FILE_IDS = {1: "frontend.cu", 2: "rowops.cu", 3: "gemm.cu", 4: "attention.cu", 5: "ctc.cu",
-            6: "window_attention.cu", 7: "paged_attention.cu", 8: "cache.cu"}
+            6: "window_attention.cu", 7: "paged_attention.cu", 8: "cache.cu", 9: "stream.cu"}
 
 
 def check_report() -> dict:
@@ -711,9 +719,9 @@ class PagedCache:
         return out, out.record.table, out.record.lengths
 
 
-def sal_cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor,
+def sal_cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor | None,
                      seqs: torch.Tensor | None = None, layer: int = 0, stream=None) -> None:
-    """k, v [batch, kv_heads, T, head_dim] bf16 into positions starts[b] + t of sequences seqs[b] (None: b)."""
+    """k, v [batch, kv_heads, T, head_dim] bf16 into positions starts[b] + t (None: t) of sequences seqs[b] (None: b)."""
     B, kvh, T, hd = k.shape
     if (kvh, hd) != (cache.record.kv_heads, cache.record.head_dim):
         raise ValueError(f"k: the cache has {cache.record.kv_heads} heads of {cache.record.head_dim}")
@@ -785,3 +793,48 @@ def sal_attention_paged(q: torch.Tensor, cache: PagedCache, left: int = -1, sink
         ctypes.byref(win), _operand("out", out, torch.bfloat16, (B, H * hd)),
         _operand("workspace", workspace, torch.uint8), workspace.numel(), _stream(stream)))
     return out
+
+
+def stream_workspace(batch: int, T: int = 1, device="cuda") -> torch.Tensor:
+    n = lib().sal_stream_workspace_bytes(batch, T)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def sal_stream_prefill(x: torch.Tensor, weights, n_layers: int, cache: PagedCache, left: int = -1, sinks: int = 0,
+                       lengths: torch.Tensor | None = None, seqs: torch.Tensor | None = None,
+                       emb: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                       stream=None) -> torch.Tensor:
+    """x [batch, T, 1280] float32 (clobbered): the first positions of live streams -> emb [batch, T, 1280] bf16, their
+    keys and values kept in the cache (resize the sequences first)."""
+    rec = weights.record if isinstance(weights, DeviceWeights) else weights
+    B, T, width = x.shape
+    if emb is None:
+        emb = torch.empty((B, T, width), dtype=torch.bfloat16, device=x.device)
+    if workspace is None:
+        workspace = stream_workspace(B, T, x.device)
+    win = sal_window(left, 0, sinks)
+    _check("sal_stream_prefill", lib().sal_stream_prefill(
+        _operand("x", x, torch.float32, (B, T, WIDTH)), B, T, _list_operand("lengths", lengths, B), ctypes.byref(rec),
+        n_layers, ctypes.byref(win), cache.ref, _list_operand("seqs", seqs, B),
+        _operand("emb", emb, torch.bfloat16, x.shape), _operand("workspace", workspace, torch.uint8),
+        workspace.numel(), _stream(stream)))
+    return emb
+
+
+def sal_stream_step(x: torch.Tensor, weights, n_layers: int, cache: PagedCache, left: int = -1, sinks: int = 0,
+                    seqs: torch.Tensor | None = None, emb: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """x [batch, 1280] float32 (clobbered): one new position of each live stream -> emb [batch, 1280] bf16 (make the
+    sequences longer by one first, with sal_cache_resize)."""
+    rec = weights.record if isinstance(weights, DeviceWeights) else weights
+    B, width = x.shape
+    if emb is None:
+        emb = torch.empty((B, width), dtype=torch.bfloat16, device=x.device)
+    if workspace is None:
+        workspace = stream_workspace(B, 1, x.device)
+    win = sal_window(left, 0, sinks)
+    _check("sal_stream_step", lib().sal_stream_step(
+        _operand("x", x, torch.float32, (B, WIDTH)), B, ctypes.byref(rec), n_layers, ctypes.byref(win), cache.ref,
+        _list_operand("seqs", seqs, B), _operand("emb", emb, torch.bfloat16, x.shape),
+        _operand("workspace", workspace, torch.uint8), workspace.numel(), _stream(stream)))
+    return emb

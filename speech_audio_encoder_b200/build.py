@@ -23,7 +23,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsal.so")
 LIB_CHECKED = os.path.join(PKG, "libsal_checked.so")
 SOURCES = ["sal_api.cu", "frontend.cu", "rowops.cu", "gemm.cu", "attention.cu", "noalloc.cu", "ctc.cu",
-           "weights_io.cu", "window_attention.cu", "paged_attention.cu", "cache.cu"]
+           "weights_io.cu", "window_attention.cu", "paged_attention.cu", "cache.cu",
+           "stream.cu"]
 HEADERS = ["sal_internal.h", "sal_ptx.cuh", "sal_mma.cuh", "sal_check.cuh"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
   const int seq = a.seqs ? *SAL_CK_LD(a.seqs + b, 4) : b;
   if (seq < 0 || seq >= a.sequences) return;
   const int len = min(*SAL_CK_LD(a.lengths + seq, 4), a.max_pages << a.page_shift);
-  const int start = *SAL_CK_LD(a.starts + b, 4);
+  const int start = a.starts ? *SAL_CK_LD(a.starts + b, 4) : 0;
   const unsigned per_row = static_cast<unsigned>(a.kv_heads) * a.T;  // (head, token) rows of this batch row
   const unsigned i = blockIdx.x * 256u + threadIdx.x;
   const unsigned r = i >> a.row_shift, c = i & ((1u << a.row_shift) - 1);
@@ -565,7 +565,7 @@ sal_status sal_cache_append(const sal_cache* cache, int layer, const void* k, co
   if (batch > 65535 || T > (int64_t(1) << 28) || ((cache->kv_heads * T) << row_shift) > (int64_t(1) << 31))
     return SAL_ESHAPE;
   if (batch == 0 || T == 0) return SAL_OK;
-  if (!k || !v || !starts || !aligned16(k) || !aligned16(v) || !aligned4(starts) || !aligned4(seqs)) return SAL_EINVAL;
+  if (!k || !v || !aligned16(k) || !aligned16(v) || !aligned4(starts) || !aligned4(seqs)) return SAL_EINVAL;
   if (!seqs && batch > cache->sequences) return SAL_EINVAL;
   SAL_TRY(require_device());
   AppendArgs a{};

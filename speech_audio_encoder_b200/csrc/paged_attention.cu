@@ -611,6 +611,10 @@ sal_status launch(const PagedArgs& a, const Plan& p, cudaStream_t s, const std::
 }
 
 }  // namespace
+
+size_t attention_paged_bytes(int head_dim) { return workspace_bytes(head_dim); }
+size_t attention_paged_zero_bytes() { return kArrivedBytes; }
+
 }  // namespace sal
 
 extern "C" {

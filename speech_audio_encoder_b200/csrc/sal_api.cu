@@ -150,6 +150,7 @@ bool is_device_ptr(const void* p) {
 }  // namespace
 
 sal_status require_device() { return check_device(); }
+bool layer_parameters_ok(const sal_layer& L) { return layer_ok(L); }
 
 uint64_t wait_limit_ns() { return g_wait_limit_ns.load(); }
 

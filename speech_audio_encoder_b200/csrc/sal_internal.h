@@ -49,6 +49,7 @@ struct NvtxRange {
 };
 
 sal_status require_device();  // SAL_OK when the current device is an sm_100 GPU
+bool layer_parameters_ok(const sal_layer& L);  // no null or misaligned parameter
 uint64_t wait_limit_ns();
 bool pdl_enabled();  // programmatic dependent launch (env SAL_PDL=0 turns it off)
 void count_launch();  // one kernel enqueued
@@ -111,6 +112,10 @@ sal_status log_softmax_launch(const float* z, int64_t rows, int n, int64_t ld, f
 sal_status window_attention_launch(const void* q, const void* k, const void* v, int batch, int64_t T, int heads,
                                    int kv_heads, int head_dim, const sal_window& win, const int32_t* lengths, void* o,
                                    cudaStream_t s);
+
+// paged_attention.cu: bytes of its workspace, and how many of them (the first) have to start as zeros
+size_t attention_paged_bytes(int head_dim);
+size_t attention_paged_zero_bytes();
 
 // cache.cu
 sal_status check_cache(const sal_cache* c, bool workspace);  // the members of a cache record

@@ -80,7 +80,7 @@ def test_cache_call_refusals(api):
     append = lambda layer=0, k=4096, v=4096, b=1, T=1, st=4096, sq=0: lib.sal_cache_append(r, layer, k, v, b, T, st, sq, 0)  # noqa: E731,E501
     assert append(layer=2) == EINVAL and append(layer=-1) == EINVAL and append(b=-1) == EINVAL and append(T=-1) == EINVAL
     assert append(b=0) == OK and append(T=0) == OK
-    assert append(k=0) == EINVAL and append(v=4104) == EINVAL and append(st=0) == EINVAL and append(st=4097) == EINVAL
+    assert append(k=0) == EINVAL and append(v=4104) == EINVAL and append(st=4097) == EINVAL and append(sq=4098) == EINVAL
     assert append(b=5) == EINVAL            # five rows without a list, four sequences
     assert append(b=65536, sq=4096) == ESHAPE and append(T=(1 << 28) + 1) == ESHAPE
     assert append(T=(1 << 26) + 1) == ESHAPE  # 2 heads x T x 16 vectors past 2^31
@@ -130,6 +130,34 @@ def test_paged_attention_refusals(api):
         assert call(**bad) == EINVAL, bad
     assert call(batch=65536, seqs=4096) == ESHAPE and call(heads=65536) == ESHAPE
     assert call(bytes=n - 1) == EWORKSPACE
+
+
+def test_stream_refusals(api):
+    """The live-stream encoder: the encoder's own checks, and a cache of its heads and layers."""
+    lib = api.lib()
+    layers = (api.sal_layer * 2)(*[api.sal_layer(*[4096] * len(api.LAYER_FIELDS)) for _ in range(2)])
+    w = api.sal_weights(4096, 4096, layers, 2, 4096, 4096)
+    good = dict(kv_heads=10, head_dim=128, layers=2)
+    n1, n8 = lib.sal_stream_workspace_bytes(3, 1), lib.sal_stream_workspace_bytes(3, 8)
+    assert lib.sal_stream_workspace_bytes(0, 8) == 0 and lib.sal_stream_workspace_bytes(3, 0) == 0
+    assert n8 >= 24 * 1280 * 2 * 5 and n1 >= 3 * (1280 * 2 * 5 + 3840 * 4)
+
+    def both(cache=None, x=4096, batch=3, T=8, n=2, sinks=0, emb=4096, ws=4096, b1=n1, b8=n8, seqs=0, weights=w, lens=0):
+        c = _cache(api, **(good if cache is None else cache))
+        r, wr, win = ctypes.byref(c), ctypes.byref(weights), _window(api, left=5, sinks=sinks)
+        return (lib.sal_stream_prefill(x, batch, T, lens, wr, n, win, r, seqs, emb, ws, b8, 0),
+                lib.sal_stream_step(x, batch, wr, n, win, r, seqs, emb, ws, b1, 0))
+
+    for change, want in ((dict(batch=-1), EINVAL), (dict(n=-1), EINVAL), (dict(n=3), EINVAL), (dict(sinks=-1), EINVAL),
+                         (dict(x=0), EINVAL), (dict(x=4104), EINVAL), (dict(emb=0), EINVAL), (dict(ws=0), EINVAL),
+                         (dict(ws=4096 + 64), EINVAL), (dict(seqs=4098), EINVAL), (dict(batch=5), EINVAL),
+                         (dict(batch=6554, seqs=4096), ESHAPE), (dict(batch=0), OK), (dict(b1=n1 - 1, b8=n8 - 1), EWORKSPACE),
+                         (dict(cache=dict(good, kv_heads=2)), ESHAPE), (dict(cache=dict(good, head_dim=64)), ESHAPE),
+                         (dict(cache=dict(good, layers=1)), ESHAPE), (dict(cache=dict(good, page_size=24)), ESHAPE)):
+        assert both(**change) == (want, want), change
+    assert both(T=45001)[0] == ESHAPE and both(T=-1)[0] == EINVAL and both(T=0)[0] == OK and both(lens=4098)[0] == EINVAL
+    layers[1].w_o = 0
+    assert both() == (EINVAL, EINVAL)
 
 
 # ----------------------------------------------------------------- the model of the tables
