@@ -484,6 +484,12 @@ sal_status sal_attention_window(const void* q, const void* k, const void* v, int
                                 int kv_heads, int head_dim, const sal_window* window, const int32_t* lengths,
                                 void* o, void* stream);
 
+/* Test hook for that kernel's bounded waits, as sal_attention_withhold: sal_attention_window
+ * over `heads` heads of their own keys, except that of every query tile pair's key tiles none
+ * from number `tile` on is loaded. Errors: as sal_attention_window, and SAL_EINVAL for tile < 0. */
+sal_status sal_attention_window_withhold(const void* q, const void* k, const void* v, int batch, int64_t T, int heads,
+                                         int head_dim, const sal_window* window, int tile, void* o, void* stream);
+
 #define SAL_CACHE_MAX_PAGES 524288
 #define SAL_CACHE_MAX_SEQUENCES 32768
 

@@ -154,6 +154,10 @@ EXPORTS = {
                                              ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                              ctypes.POINTER(sal_window), ctypes.c_void_p, ctypes.c_void_p,
                                              ctypes.c_void_p]),
+    "sal_attention_window_withhold": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                                      ctypes.c_int64, ctypes.c_int, ctypes.c_int,
+                                                      ctypes.POINTER(sal_window), ctypes.c_int, ctypes.c_void_p,
+                                                      ctypes.c_void_p]),
     "sal_cache_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int]),
     "sal_cache_append": (ctypes.c_int, [ctypes.POINTER(sal_cache), ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
                                          ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
@@ -658,6 +662,19 @@ def sal_attention_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, left
         T, H, kvh, hd, ctypes.byref(win), _list_operand("lengths", lengths, B),
         _operand("out", out, torch.bfloat16, (B * T, H * hd)), _stream(stream)))
     return out
+
+
+def sal_attention_window_withhold(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tile: int, left: int = -1,
+                                  right: int = -1, sinks: int = 0, stream=None) -> torch.Tensor:
+    """Test hook: sal_attention_window with no key tile from ``tile`` on ever loaded, so a bounded wait gives up (read
+    the outcome with sal_last_device_status)."""
+    B, H, T, hd = q.shape
+    o = torch.empty((B * T, H * hd), dtype=torch.bfloat16, device=q.device)
+    win = sal_window(left, right, sinks)
+    _check("sal_attention_window_withhold", lib().sal_attention_window_withhold(
+        _operand("q", q, torch.bfloat16), _operand("k", k, torch.bfloat16, q.shape),
+        _operand("v", v, torch.bfloat16, q.shape), B, T, H, hd, ctypes.byref(win), tile, o.data_ptr(), _stream(stream)))
+    return o
 
 
 class PagedCache:

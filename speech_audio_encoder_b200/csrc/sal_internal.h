@@ -111,7 +111,7 @@ sal_status log_softmax_launch(const float* z, int64_t rows, int n, int64_t ld, f
 // window_attention.cu
 sal_status window_attention_launch(const void* q, const void* k, const void* v, int batch, int64_t T, int heads,
                                    int kv_heads, int head_dim, const sal_window& win, const int32_t* lengths, void* o,
-                                   cudaStream_t s);
+                                   cudaStream_t s, int withhold = -1);
 
 // paged_attention.cu: bytes of its workspace, and how many of them (the first) have to start as zeros
 size_t attention_paged_bytes(int head_dim);

@@ -76,6 +76,7 @@ struct WindowArgs {
   float scale_log2;
   uint64_t limit_ns;
   unsigned int* status;
+  int withhold = -1;       // test hook: key tile of every item from which on no key is loaded
 };
 
 // One work item: up to two query tiles and the key tiles they share. Its first tiles hold the
@@ -459,11 +460,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       // keys, and behind an item's first tile its queries, as soon as the last S before has read its slot's
-      for (int k = 0; ok; ++k) {
+      bool go = true;
+      for (int k = 0; ok && go; ++k) {
         if (!(ok = item_ready(k))) break;
         const Item& it = items[k % kItems];
         if (it.count == 0) break;
         for (int x = 0; ok && x < it.count; ++x) {
+          if (!(go = x != args.withhold)) break;
           const uint32_t s = loads_k % NK;
           if (!(ok = mbar_sleep(&k_empty[s], ((loads_k / NK) & 1) ^ 1, guard))) break;
           mbar_arrive_expect_tx(&k_full[s], L::kKB);
@@ -725,7 +728,7 @@ int ready_sms() {
 
 sal_status window_attention_launch(const void* q, const void* k, const void* v, int batch, int64_t T, int heads,
                                    int kv_heads, int head_dim, const sal_window& win, const int32_t* lengths, void* o,
-                                   cudaStream_t s) {
+                                   cudaStream_t s, int withhold) {
   const int sms = ready_sms();
   if (!sms) return SAL_ECUDA;
   WindowArgs a{};
@@ -743,6 +746,7 @@ sal_status window_attention_launch(const void* q, const void* k, const void* v, 
   a.wide = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
   a.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(head_dim));
   a.limit_ns = wait_limit_ns();
+  a.withhold = withhold;
   a.status = device_status_ptr();
   if (!a.status) return SAL_ECUDA;
   const int planes = batch * heads;
@@ -774,11 +778,11 @@ sal_status window_attention_launch(const void* q, const void* k, const void* v, 
 
 }  // namespace sal
 
-extern "C" sal_status sal_attention_window(const void* q, const void* k, const void* v, int batch, int64_t T,
-                                           int heads, int kv_heads, int head_dim, const sal_window* window,
-                                           const int32_t* lengths, void* o, void* stream) {
+namespace {
+sal_status attention_window(const void* q, const void* k, const void* v, int batch, int64_t T, int heads, int kv_heads,
+                            int head_dim, const sal_window* window, const int32_t* lengths, void* o, void* stream,
+                            int withhold) {
   using namespace sal;
-  const NvtxRange nvtx_("sal_attention_window");
   if (batch < 0 || T < 0 || heads < 0 || kv_heads < 0) return SAL_EINVAL;
   if (window && window->sinks < 0) return SAL_EINVAL;
   if (head_dim != 64 && head_dim != 128) return SAL_ESHAPE;
@@ -793,5 +797,22 @@ extern "C" sal_status sal_attention_window(const void* q, const void* k, const v
   if (st != SAL_OK) return st;
   const sal_window all{-1, -1, 0};
   return window_attention_launch(q, k, v, batch, T, heads, kv_heads, head_dim, window ? *window : all, lengths, o,
-                                 static_cast<cudaStream_t>(stream));
+                                 static_cast<cudaStream_t>(stream), withhold);
+}
+}  // namespace
+
+extern "C" sal_status sal_attention_window(const void* q, const void* k, const void* v, int batch, int64_t T,
+                                           int heads, int kv_heads, int head_dim, const sal_window* window,
+                                           const int32_t* lengths, void* o, void* stream) {
+  const sal::NvtxRange nvtx_("sal_attention_window");
+  return attention_window(q, k, v, batch, T, heads, kv_heads, head_dim, window, lengths, o, stream, -1);
+}
+
+// Test hook: no key tile of an item from `tile` on is loaded, so that bounded waits give up (see sal.h).
+extern "C" sal_status sal_attention_window_withhold(const void* q, const void* k, const void* v, int batch, int64_t T,
+                                                    int heads, int head_dim, const sal_window* window, int tile,
+                                                    void* o, void* stream) {
+  const sal::NvtxRange nvtx_("sal_attention_window_withhold");
+  if (tile < 0) return SAL_EINVAL;
+  return attention_window(q, k, v, batch, T, heads, heads, head_dim, window, nullptr, o, stream, tile);
 }

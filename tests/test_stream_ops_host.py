@@ -38,6 +38,14 @@ def test_window_attention_refusals(api, change, want):
                                           0) == want
 
 
+def test_window_withhold_refusals(api):
+    f = api.lib().sal_attention_window_withhold
+    assert f(4096, 4096, 4096, 1, 512, 4, 128, None, -1, 4096, 0) == EINVAL
+    assert f(4096, 4096, 4096, 1, 512, 4, 96, None, 1, 4096, 0) == ESHAPE
+    assert f(0, 4096, 4096, 1, 512, 4, 128, None, 1, 4096, 0) == EINVAL
+    assert f(4096, 4096, 4096, 1, 0, 4, 128, None, 1, 4096, 0) == OK
+
+
 def _cache(api, **change):
     c = dict(k=4096, v=4096, layers=2, pages=64, kv_heads=2, page_size=16, head_dim=128, sequences=4, max_pages=8,
              table=4096, lengths=4096, status=4096, workspace=4096, workspace_bytes=1 << 20)
