@@ -208,7 +208,7 @@ def _load(path: str) -> ctypes.CDLL:
 def lib() -> ctypes.CDLL:
     """The loaded library (libsal.so, or libsal_checked.so inside `checked_library()` or
     with SAL_LIB=checked). Raises if it has not been built."""
-    return _load(_active)
+    return _libs.get(_active) or _load(_active)
 
 
 @contextlib.contextmanager
@@ -623,12 +623,26 @@ def attention_plan(batch: int, T: int, heads: int = 10, head_dim: int = 128, sms
 
 # ----------------------------------------------------------------------------- live streams
 
+_current_device = torch._C._cuda_getDevice
+_windows: dict = {}
+
+
+def _window(left: int, right: int, sinks: int):
+    """The sal_window of these limits, by reference (made once: a step of a stream asks for the same one every time)."""
+    w = _windows.get((left, right, sinks))
+    if w is None:
+        if len(_windows) > 1000:
+            _windows.clear()
+        w = _windows[(left, right, sinks)] = ctypes.byref(sal_window(left, right, sinks))
+    return w
+
+
 def _operand(name: str, t: torch.Tensor, dtype, shape=None) -> int:
     """The address of a contiguous tensor of this type (and shape) on the current device."""
     if t.dtype is not dtype or (shape is not None and t.shape != shape):
         raise ValueError(f"{name}: expected {dtype}{'' if shape is None else ' of shape ' + str(tuple(shape))}, got "
                          f"{t.dtype} of shape {tuple(t.shape)}")
-    if t.get_device() != torch._C._cuda_getDevice():
+    if t.get_device() != _current_device():
         raise ValueError(f"{name}: must be on the current CUDA device")
     if not t.is_contiguous():
         raise ValueError("tensors passed to libsal must be contiguous")
@@ -656,10 +670,9 @@ def sal_attention_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, left
     if out is None:
         out = (torch.empty if lengths is None else torch.zeros)((B * T, H * hd), dtype=torch.bfloat16, device=q.device)
     kv = (B, kvh, T, hd)
-    win = sal_window(left, right, sinks)
     _check("sal_attention_window", lib().sal_attention_window(
         _operand("q", q, torch.bfloat16), _operand("k", k, torch.bfloat16, kv), _operand("v", v, torch.bfloat16, kv), B,
-        T, H, kvh, hd, ctypes.byref(win), _list_operand("lengths", lengths, B),
+        T, H, kvh, hd, _window(left, right, sinks), _list_operand("lengths", lengths, B),
         _operand("out", out, torch.bfloat16, (B * T, H * hd)), _stream(stream)))
     return out
 
@@ -670,10 +683,9 @@ def sal_attention_window_withhold(q: torch.Tensor, k: torch.Tensor, v: torch.Ten
     the outcome with sal_last_device_status)."""
     B, H, T, hd = q.shape
     o = torch.empty((B * T, H * hd), dtype=torch.bfloat16, device=q.device)
-    win = sal_window(left, right, sinks)
     _check("sal_attention_window_withhold", lib().sal_attention_window_withhold(
         _operand("q", q, torch.bfloat16), _operand("k", k, torch.bfloat16, q.shape),
-        _operand("v", v, torch.bfloat16, q.shape), B, T, H, hd, ctypes.byref(win), tile, o.data_ptr(), _stream(stream)))
+        _operand("v", v, torch.bfloat16, q.shape), B, T, H, hd, _window(left, right, sinks), tile, o.data_ptr(), _stream(stream)))
     return o
 
 
@@ -697,12 +709,14 @@ class PagedCache:
             workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=k.device)
         self.k, self.v, self.table, self.lengths = k, v, table, lengths
         self.status, self.workspace = status, workspace
+        self.kv_heads, self.head_dim = kv_heads, head_dim
         self.record = sal_cache(
             _operand("k", k, torch.bfloat16), _operand("v", v, torch.bfloat16, k.shape), layers, pages, kv_heads,
             page_size, head_dim, sequences, max_pages, _operand("table", table, torch.int32),
             _operand("lengths", lengths, torch.int32, (sequences,)), _operand("status", status, torch.int32, (1,)),
             _operand("workspace", workspace, torch.uint8), workspace.numel())
         self.ref = ctypes.byref(self.record)
+        self.pool, self.places = k.data_ptr(), (self.record.table, self.record.lengths)
 
     @classmethod
     def empty(cls, layers: int, pages: int, kv_heads: int, page_size: int, head_dim: int, sequences: int,
@@ -730,18 +744,19 @@ class PagedCache:
             raise RuntimeError("cache operation failed: " + "; ".join(what))
 
     def _tables_of(self, out: "PagedCache | None") -> tuple:
-        out = self if out is None else out
-        if out.table.shape != self.table.shape or out.k.data_ptr() != self.k.data_ptr():
+        if out is None:
+            return self, *self.places
+        if out.table.shape != self.table.shape or out.pool != self.pool:
             raise ValueError("out: must be this cache's pages under tables of the same shape")
-        return out, out.record.table, out.record.lengths
+        return out, *out.places
 
 
 def sal_cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor | None,
                      seqs: torch.Tensor | None = None, layer: int = 0, stream=None) -> None:
     """k, v [batch, kv_heads, T, head_dim] bf16 into positions starts[b] + t (None: t) of sequences seqs[b] (None: b)."""
     B, kvh, T, hd = k.shape
-    if (kvh, hd) != (cache.record.kv_heads, cache.record.head_dim):
-        raise ValueError(f"k: the cache has {cache.record.kv_heads} heads of {cache.record.head_dim}")
+    if kvh != cache.kv_heads or hd != cache.head_dim:
+        raise ValueError(f"k: the cache has {cache.kv_heads} heads of {cache.head_dim}")
     _check("sal_cache_append", lib().sal_cache_append(
         cache.ref, layer, _operand("k", k, torch.bfloat16), _operand("v", v, torch.bfloat16, k.shape), B, T,
         _list_operand("starts", starts, B), _list_operand("seqs", seqs, B), _stream(stream)))
@@ -770,9 +785,8 @@ def sal_cache_resize(cache: PagedCache, seqs: torch.Tensor, new_lengths: torch.T
     position sees are let go. The new tables go to ``out`` (None: in place)."""
     out, table, lengths = cache._tables_of(out)
     n = seqs.shape[0]
-    win = sal_window(left, 0, sinks)
     _check("sal_cache_resize", lib().sal_cache_resize(
-        cache.ref, _list_operand("seqs", seqs), _list_operand("new_lengths", new_lengths, n), n, ctypes.byref(win),
+        cache.ref, _list_operand("seqs", seqs), _list_operand("new_lengths", new_lengths, n), n, _window(left, 0, sinks),
         table, lengths, _stream(stream)))
     return out
 
@@ -796,18 +810,18 @@ def sal_attention_paged(q: torch.Tensor, cache: PagedCache, left: int = -1, sink
     """q [batch, heads, head_dim] bf16 (any strides of its first two dimensions that are multiples of 8), the newest
     position of sequences seqs[b] (None: b) -> o [batch, heads * head_dim]."""
     B, H, hd = q.shape
-    if hd != cache.record.head_dim or q.stride(2) != 1:
-        raise ValueError(f"q: expected contiguous heads of {cache.record.head_dim}")
-    if q.dtype is not torch.bfloat16 or not q.is_cuda or q.device.index != torch.cuda.current_device():
+    rows, heads, inner = q.stride()
+    if hd != cache.head_dim or inner != 1:
+        raise ValueError(f"q: expected contiguous heads of {cache.head_dim}")
+    if q.dtype is not torch.bfloat16 or q.get_device() != _current_device():
         raise ValueError("q: expected bfloat16 on the current CUDA device")
     if out is None:
         out = torch.empty((B, H * hd), dtype=torch.bfloat16, device=q.device)
     if workspace is None:
         workspace = attention_paged_workspace(cache, B, H)
-    win = sal_window(left, 0, sinks)
     _check("sal_attention_paged", lib().sal_attention_paged(
-        q.data_ptr(), q.stride(0), q.stride(1), B, H, cache.ref, layer, _list_operand("seqs", seqs, B),
-        ctypes.byref(win), _operand("out", out, torch.bfloat16, (B, H * hd)),
+        q.data_ptr(), rows, heads, B, H, cache.ref, layer, 0 if seqs is None else _list_operand("seqs", seqs, B),
+        _window(left, 0, sinks), _operand("out", out, torch.bfloat16, (B, H * hd)),
         _operand("workspace", workspace, torch.uint8), workspace.numel(), _stream(stream)))
     return out
 
@@ -829,10 +843,9 @@ def sal_stream_prefill(x: torch.Tensor, weights, n_layers: int, cache: PagedCach
         emb = torch.empty((B, T, width), dtype=torch.bfloat16, device=x.device)
     if workspace is None:
         workspace = stream_workspace(B, T, x.device)
-    win = sal_window(left, 0, sinks)
     _check("sal_stream_prefill", lib().sal_stream_prefill(
         _operand("x", x, torch.float32, (B, T, WIDTH)), B, T, _list_operand("lengths", lengths, B), ctypes.byref(rec),
-        n_layers, ctypes.byref(win), cache.ref, _list_operand("seqs", seqs, B),
+        n_layers, _window(left, 0, sinks), cache.ref, _list_operand("seqs", seqs, B),
         _operand("emb", emb, torch.bfloat16, x.shape), _operand("workspace", workspace, torch.uint8),
         workspace.numel(), _stream(stream)))
     return emb
@@ -849,9 +862,8 @@ def sal_stream_step(x: torch.Tensor, weights, n_layers: int, cache: PagedCache, 
         emb = torch.empty((B, width), dtype=torch.bfloat16, device=x.device)
     if workspace is None:
         workspace = stream_workspace(B, 1, x.device)
-    win = sal_window(left, 0, sinks)
     _check("sal_stream_step", lib().sal_stream_step(
-        _operand("x", x, torch.float32, (B, WIDTH)), B, ctypes.byref(rec), n_layers, ctypes.byref(win), cache.ref,
+        _operand("x", x, torch.float32, (B, WIDTH)), B, ctypes.byref(rec), n_layers, _window(left, 0, sinks), cache.ref,
         _list_operand("seqs", seqs, B), _operand("emb", emb, torch.bfloat16, x.shape),
         _operand("workspace", workspace, torch.uint8), workspace.numel(), _stream(stream)))
     return emb

@@ -443,7 +443,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  pdl_wait();
   pdl_trigger();
   const uint32_t tmem = *tmem_slot;
   const WaitGuard guard{abort_flag, args.limit_ns, args.status};
@@ -458,6 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     setmaxnreg_dec<kRegsCtrl>();
   if (warp == 0) {
+    pdl_wait();  // (each role waits for the kernel before where it first touches memory)
     if (lane == 0) {
       // keys, and behind an item's first tile its queries, as soon as the last S before has read its slot's
       bool go = true;
@@ -491,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 2) {
     drain_products(&sm.drains[1], issue_outputs<HD>(args, sm, guard, tmem), guard);
   } else if (warp == 3) {
+    if (args.lengths) pdl_wait();
     if (lane == 0) {
       // works the items out one ahead of the other roles (those past a clip's end are left out, an
       // item of no tiles is the end), and loads the values: a thread of its own, so that a key tile
@@ -513,6 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = mbar_sleep(&item_empty[at], (((k + 1) / kItems) & 1) ^ 1, guard))) break;
         items[at] = next;
         mbar_arrive(&item_full[at]);
+        if (k < 0) pdl_wait();
         if (k >= 0) {
           for (int x = 0; ok && x < now.count; ++x) {
             const uint32_t s = loads_v % NV;
@@ -530,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   } else {
     setmaxnreg_inc<kRegsSoftmax>();
+    pdl_wait();
     const int slot = (warp - 4) >> 2, quarter = warp & 3;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t colS = tmem + lane_base + L::col_s(slot), colP = tmem + lane_base + L::col_p(slot);
