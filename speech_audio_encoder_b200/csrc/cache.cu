@@ -23,7 +23,7 @@ namespace sal {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-constexpr int kForkInts = 49152;  // shared-memory ints of a fork block's tile
+constexpr int kForkInts = 32768;  // shared-memory ints of a fork block's tile: one column of the longest list
 
 struct TableArgs {
   const int32_t *table, *lengths;
@@ -620,7 +620,8 @@ sal_status sal_cache_fork(const sal_cache* cache, const int32_t* src, const int3
   SAL_TRY(require_device());
   SAL_TRY(kernel_attributes());
   const TableArgs t = table_args(cache, table_out, lengths_out);
-  const int cols = std::max(1, std::min(32, n > 0 ? kForkInts / n : 32));
+  // as many blocks as keep a thread at one or two entries of the list's columns
+  const int cols = std::max(1, std::min(32, n > 0 ? 512 / n : 32));
   declare_tables(t);
   ck_declare(src, static_cast<uint64_t>(n) * 4, false);
   ck_declare(dst, static_cast<uint64_t>(n) * 4, false);

@@ -261,22 +261,45 @@ __device__ __forceinline__ void walk(const PagedArgs& a, const Span& sp, int seq
   __syncthreads();
 }
 
-// Column d of row r over the warps' results: the sum, the maximum it is relative to, the total weight.
+// The warps' results of a walk into one: a weight for every warp and row, and the row's maximum and
+// total weight, worked out once (by a thread per row) for all columns. All threads call it.
+struct Merged {
+  float weight[kRowTile][kWarps], top[kRowTile], total[kRowTile];
+};
 template <int HD>
-__device__ __forceinline__ void merge_warps(const uint8_t* smem, int r, int d, float& x, float& mm, float& total) {
-  const float* so = reinterpret_cast<const float*>(smem);
-  const float* sml = so + kWarps * kRowTile * Ring<HD>::kPitch;
-  mm = -INFINITY;
-  x = total = 0.f;
+__device__ __forceinline__ void merge_weights(const uint8_t* smem, int rows, Merged& m) {
+  const float* sml = reinterpret_cast<const float*>(smem) + kWarps * kRowTile * Ring<HD>::kPitch;
+  const int r = threadIdx.x;
+  if (r < rows) {
+    float mm = -INFINITY, total = 0.f;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sml[2 * (w * kRowTile + r)]);
+    for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sml[2 * (w * kRowTile + r)]);
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int at = w * kRowTile + r;
-    const float f = sml[2 * at + 1] > 0.f ? fast_exp2(sml[2 * at] - mm) : 0.f;
-    total += sml[2 * at + 1] * f;
-    x += so[at * Ring<HD>::kPitch + d] * f;
+    for (int w = 0; w < kWarps; ++w) {
+      const int at = w * kRowTile + r;
+      const float f = sml[2 * at + 1] > 0.f ? fast_exp2(sml[2 * at] - mm) : 0.f;
+      total += sml[2 * at + 1] * f;
+      m.weight[r][w] = f;
+    }
+    m.top[r] = mm;
+    m.total[r] = total;
   }
+  __syncthreads();
+}
+// Column d of row r, relative to its maximum.
+template <int HD>
+__device__ __forceinline__ float merged(const uint8_t* smem, const Merged& m, int r, int d) {
+  const float* so = reinterpret_cast<const float*>(smem) + r * Ring<HD>::kPitch + d;
+  float x = 0.f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) x = fmaf(so[w * kRowTile * Ring<HD>::kPitch], m.weight[r][w], x);
+  return x;
+}
+
+// a / b for a >= 0, b > 0: in 32 bits where they fit (a tenth of the 64-bit division's time).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
 
 template <int HD>
@@ -300,13 +323,14 @@ __global__ void __launch_bounds__(kThreads, 2) paged_cluster_kernel(const PagedA
   const int seq = a.seqs ? *SAL_CK_LD(a.seqs + b, 4) : b;
   const Span sp = span_of(a, seq);
   walk<HD>(a, sp, seq, b, kvh, h0, rows, sp.blocks * split / a.splits, sp.blocks * (split + 1) / a.splits, smem);
+  __shared__ Merged mg;
+  merge_weights<HD>(smem, rows, mg);
   // each thread: one column of every (128 / HD)-th row
   float* so = reinterpret_cast<float*>(smem);
   float* sml = so + kWarps * kRowTile * R::kPitch + 2 * kWarps * kRowTile;  // behind the warps' pairs
   const int d = threadIdx.x % HD;
   for (int r = threadIdx.x / HD; r < rows; r += kThreads / HD) {
-    float x, mm, total;
-    merge_warps<HD>(smem, r, d, x, mm, total);
+    const float x = merged<HD>(smem, mg, r, d), mm = mg.top[r], total = mg.total[r];
     if (a.splits == 1) {
       store_out<HD>(a, b, h0 + r, d, x, total);
       continue;
@@ -346,6 +370,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_line_kernel(const PagedArgs
   __shared__ int64_t sums[kWarps];
   __shared__ int64_t found[2];  // where the part's first row begins, and which row it is
   __shared__ int last_here;
+  __shared__ Merged mg;
   const int tid = threadIdx.x, groups = a.kv_heads * a.row_tiles, share = a.heads / a.kv_heads;
   pdl_wait();
   pdl_trigger();
@@ -372,10 +397,14 @@ __global__ void __launch_bounds__(kThreads, 2) paged_line_kernel(const PagedArgs
   // parts of at least kFewKeys blocks
   const int parts = static_cast<int>(min(static_cast<int64_t>(gridDim.x), (units + kFewKeys - 1) / kFewKeys));
   const int c = blockIdx.x;
-  const int64_t u0 = c < parts ? units * c / parts : 0, u1 = c < parts ? units * (c + 1) / parts : 0;
+  const int64_t u0 = c < parts ? quotient(units * c, parts) : 0, u1 = c < parts ? quotient(units * (c + 1), parts) : 0;
   if (u0 < u1 && u0 >= before * groups && u0 < (before + mine) * groups) {
     int64_t at = before * groups;
-    for (int b = b0; b < b1; ++b) {
+    if (per == 1) {  // this thread's only row
+      found[0] = at;
+      found[1] = b0;
+    }
+    for (int b = b0; per > 1 && b < b1; ++b) {
       const int64_t n = static_cast<int64_t>(span_of(a, seq_of(b)).blocks) * groups;
       if (u0 < at + n) {
         found[0] = at;
@@ -398,18 +427,19 @@ __global__ void __launch_bounds__(kThreads, 2) paged_line_kernel(const PagedArgs
         ++b;
         continue;
       }
-      const int group = static_cast<int>((u - at) / sp.blocks);
+      const int group = static_cast<int>(quotient(u - at, sp.blocks));
       const int64_t begin = at + static_cast<int64_t>(group) * sp.blocks;
       const int lo = static_cast<int>(u - begin), hi = static_cast<int>(min(static_cast<int64_t>(sp.blocks), u1 - begin));
       const int kvh = group / a.row_tiles, r0 = (group - kvh * a.row_tiles) * kRowTile;
       const int rows = min(kRowTile, share - r0), h0 = kvh * share + r0;
       walk<HD>(a, sp, seq, b, kvh, h0, rows, lo, hi, smem);
+      merge_weights<HD>(smem, rows, mg);
       const bool whole = lo == 0 && hi == sp.blocks;
       // the part that holds unit v: units * e / parts <= v < units * (e + 1) / parts
       auto part_of = [&](int64_t v) {
-        int64_t e = v * parts / units;
-        while (units * (e + 1) / parts <= v) ++e;
-        while (units * e / parts > v) --e;
+        int64_t e = quotient(v * parts, units);
+        while (quotient(units * (e + 1), parts) <= v) ++e;
+        while (quotient(units * e, parts) > v) --e;
         return static_cast<int>(e);
       };
       const int from = whole || lo == 0 ? c : part_of(begin);
@@ -421,8 +451,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_line_kernel(const PagedArgs
       }
       const int d = tid % HD;
       for (int r = tid / HD; r < rows; r += kThreads / HD) {
-        float x, mm, total;
-        merge_warps<HD>(smem, r, d, x, mm, total);
+        const float x = merged<HD>(smem, mg, r, d), mm = mg.top[r], total = mg.total[r];
         if (whole) {
           store_out<HD>(a, b, h0 + r, d, x, total);
           continue;
