@@ -247,8 +247,14 @@ struct Turn {
     hi0 = same(it.hi[0]);
     hi1 = same(it.hi[1]);
   }
-  __device__ bool uses0(int x) const { return x <= last0 && (x < first || x >= begin0); }
-  __device__ bool uses1(int x) const { return x <= last1 && (x < first || x >= begin1); }
+  // tiles of slot i, and the r-th of them
+  __device__ int tiles(int i) const { return i ? (last1 < 0 ? 0 : first + last1 + 1 - begin1) : (last0 < 0 ? 0 : first + last0 + 1 - begin0); }
+  __device__ int tile(int i, int r) const { return r < first ? r : (i ? begin1 : begin0) + r - first; }
+  // whether slot i is the last to take tile x: where both do, slot 1 unless it comes to it a turn earlier
+  __device__ bool frees(int i, int x, int lag) const {
+    const bool other = i ? x <= last0 && (x < first || x >= begin0) : x <= last1 && (x < first || x >= begin1);
+    return !other || i == (x < first || begin1 == begin0 + lag ? 1 : 0);
+  }
   __device__ int base(int x) const { return x < first ? kKeys * x : start + kKeys * (x - first); }
   // keys of tile x that slot i multiplies with: a multiple of 16, the rest of the tile is not used
   __device__ int cols(int i, int x) const {
@@ -256,15 +262,19 @@ struct Turn {
   }
 };
 
-// S = Q K^T for slot 0 and slot 1 in turn, tile by tile, each as soon as its buffer has been read.
-// A whole warp walks the tiles in step; one of its lanes issues.
+// S = Q K^T for slot 0 and slot 1 in turn, each for the next of its own tiles, as soon as the
+// buffer has been read. (In the order of the tiles, a tile that only one slot takes would give
+// that slot two turns in a row, and the second would hold the buffer until its softmax is done
+// with the first.) A whole warp walks in step; one of its lanes issues.
 template <int HD>
 __device__ __forceinline__ bool issue_scores(const Shared<HD>& sm, const WaitGuard& guard, uint32_t tmem) {
   using L = Layout<HD>;
   constexpr uint32_t IDESC_S = idesc_bf16(128, 0, false, false);  // + columns / 8 << 17
   const uint32_t one = elect_one();
   const uint64_t q_desc = sdesc_kmajor_sw128(smem_u32(sm.q)), k_desc = sdesc_kmajor_sw128(smem_u32(sm.k));
-  uint32_t stage = 0, par = 0, n0 = 0, n1 = 0, q0 = 0, q1 = 0;  // K stage and its parity, S products and items of each slot
+  constexpr uint32_t NK = L::kStagesK;
+  uint32_t tile0 = 0, landed = 0;                    // tiles of the items before, tiles known to have landed
+  uint32_t n0 = 0, n1 = 0, q0 = 0, q1 = 0;           // S products and items of each slot so far
   Turn t;
   for (int k = 0;; ++k) {
     if (!mbar_sleep_warp(&sm.item_full[k % kItems], (k / kItems) & 1, guard)) return false;
@@ -272,17 +282,23 @@ __device__ __forceinline__ bool issue_scores(const Shared<HD>& sm, const WaitGua
     __syncwarp();
     if (one) mbar_arrive(&sm.item_empty[k % kItems]);
     if (t.count == 0) return true;
-    bool begun0 = false, begun1 = false;
-    for (int x = 0; x < t.count; ++x) {
-      const bool u0 = t.uses0(x), u1 = t.uses1(x);
-      const uint64_t kd = k_desc + stage * (L::kKB / 16);
-      if (!mbar_sleep_warp(&sm.k_full[stage], par, guard)) return false;
+    const int tiles0 = t.tiles(0), tiles1 = t.tiles(1);
+    const int lag = L::kSharedS ? 0 : t.begin1 - t.begin0;
+    for (int turn = 0; turn < max(tiles0, tiles1 + lag); ++turn) {
 #pragma unroll 1
-      for (int i = u0 ? 0 : 1; i < (u1 ? 2 : 1); ++i) {
+      for (int i = turn < tiles0 ? 0 : 1; i < (turn >= lag && turn - lag < tiles1 ? 2 : 1); ++i) {
+        const int r = i ? turn - lag : turn;
+        const int x = t.tile(i, r);
+        const uint32_t stage = (tile0 + x) % NK, par = (tile0 + x) / NK & 1;
         const uint32_t idesc = IDESC_S | (static_cast<uint32_t>(t.cols(i, x)) >> 3 << 17), d = tmem + L::col_s(i);
-        const uint64_t qd = q_desc + i * (L::kQB / 16);
+        const uint64_t qd = q_desc + i * (L::kQB / 16), kd = k_desc + stage * (L::kKB / 16);
         const uint32_t mine = i ? n1 : n0, before = L::kSharedS ? n0 + n1 : mine;
-        if (!(i ? begun1 : begun0) && !mbar_sleep_warp(&sm.q_full[i], (i ? q1 : q0) & 1, guard)) return false;
+        const bool frees = t.frees(i, x, lag), ends = r + 1 == (i ? tiles1 : tiles0);
+        if (tile0 + x >= landed) {  // (once a tile: even a wait that is over takes about 100 clocks)
+          if (!mbar_sleep_warp(&sm.k_full[stage], par, guard)) return false;
+          landed = tile0 + x + 1;
+        }
+        if (r == 0 && !mbar_sleep_warp(&sm.q_full[i], (i ? q1 : q0) & 1, guard)) return false;
         // the scores before it have been read out of the buffer
         if (before > 0 && !mbar_sleep_warp(&sm.s_free[L::kSharedS ? 0 : i], (before - 1) & 1, guard)) return false;
         tc_fence_after();
@@ -292,29 +308,23 @@ __device__ __forceinline__ bool issue_scores(const Shared<HD>& sm, const WaitGua
                       kd + (kk >> 2) * (L::kBox / 16) + (kk & 3) * 2, idesc, kk > 0);
         umma_commit_one(one, &sm.s_full[i]);
         if (one) sm.s_issued[i] = mine + 1;
-        if (i == 1 || !u1) umma_commit_one(one, &sm.k_empty[stage]);
-        if (x == (i ? t.last1 : t.last0)) umma_commit_one(one, &sm.q_empty[i]);
-        if (i) {
+        if (frees) umma_commit_one(one, &sm.k_empty[stage]);
+        if (ends) umma_commit_one(one, &sm.q_empty[i]);
+        if (i)
           ++n1;
-          q1 += !begun1;
-          begun1 = true;
-        } else {
+        else
           ++n0;
-          q0 += !begun0;
-          begun0 = true;
-        }
-      }
-      if (++stage == L::kStagesK) {
-        stage = 0;
-        par ^= 1;
       }
     }
+    q0 += tiles0 > 0;
+    q1 += tiles1 > 0;
+    tile0 += t.count;
   }
 }
 
 // O += P V in the same order, by a warp of its own (its lanes clear the rows of V past a clip's
 // end). The tensor core runs products in the order they are issued: a slot's next S, which its
-// softmax waits for, goes ahead of its P V (unless it is not among the very next ones).
+// softmax waits for, goes ahead of its P V.
 template <int HD>
 __device__ __forceinline__ bool issue_outputs(const WindowArgs& args, const Shared<HD>& sm, const WaitGuard& guard,
                                               uint32_t tmem) {
@@ -322,7 +332,8 @@ __device__ __forceinline__ bool issue_outputs(const WindowArgs& args, const Shar
   constexpr uint32_t IDESC_O = idesc_bf16(128, HD, false, true);
   const uint32_t lane = threadIdx.x & 31, one = elect_one();
   const uint64_t v_desc = sdesc_mnmajor_sw128(smem_u32(sm.v), L::kBox);
-  uint32_t stage = 0, par = 0, n0 = 0, n1 = 0;  // V stage and its parity, P V products of each slot so far
+  constexpr uint32_t NV = L::kStagesV;
+  uint32_t tile0 = 0, landed = 0, n0 = 0, n1 = 0;  // tiles of the items before and landed; P V products of each slot
   Turn t;
   for (int k = 0;; ++k) {
     if (!mbar_sleep_warp(&sm.item_full[k % kItems], (k / kItems) & 1, guard)) return false;
@@ -331,47 +342,46 @@ __device__ __forceinline__ bool issue_outputs(const WindowArgs& args, const Shar
     __syncwarp();
     if (one) mbar_arrive(&sm.item_empty[k % kItems]);
     if (t.count == 0) return true;
-    bool begun0 = false, begun1 = false;
-    for (int x = 0; x < t.count; ++x) {
-      const bool u0 = t.uses0(x), u1 = t.uses1(x);
-      const int clear = n < args.T ? n - t.base(x) : kKeys;
-      const uint64_t vd = v_desc + stage * (L::kKB / 16);
-      if (!mbar_sleep_warp(&sm.v_full[stage], par, guard)) return false;
-      if (clear < kKeys) {
-        // rows past the clip's length hold anything (NaN times a weight of zero is NaN): zeros
-        for (int r = clear + (lane >> 3); r < kKeys; r += 4)
-          for (int b = 0; b < L::kBoxes; ++b)
-            *reinterpret_cast<uint4*>(sm.v + stage * L::kKB + b * L::kBox + r * 128 + (lane & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
+    const int tiles0 = t.tiles(0), tiles1 = t.tiles(1);
+    const int lag = L::kSharedS ? 0 : t.begin1 - t.begin0;
+    for (int turn = 0; turn < max(tiles0, tiles1 + lag); ++turn) {
 #pragma unroll 1
-      for (int i = u0 ? 0 : 1; i < (u1 ? 2 : 1); ++i) {
-        const int cols = t.cols(i, x);
+      for (int i = turn < tiles0 ? 0 : 1; i < (turn >= lag && turn - lag < tiles1 ? 2 : 1); ++i) {
+        const int r = i ? turn - lag : turn;
+        const int x = t.tile(i, r), cols = t.cols(i, x), clear = n < args.T ? n - t.base(x) : kKeys;
+        const uint32_t stage = (tile0 + x) % NV, par = (tile0 + x) / NV & 1;
+        const uint64_t vd = v_desc + stage * (L::kKB / 16);
         const uint32_t mine = i ? n1 : n0, d = tmem + L::col_o(i), pa = tmem + L::col_p(i);
-        const bool adds = i ? begun1 : begun0;
+        const bool frees = t.frees(i, x, lag), ends = r + 1 == (i ? tiles1 : tiles0);
+        if (tile0 + x >= landed) {
+          if (!mbar_sleep_warp(&sm.v_full[stage], par, guard)) return false;
+          landed = tile0 + x + 1;
+        }
+        if (clear < cols) {
+          // rows past the clip's length hold anything (NaN times a weight of zero is NaN): zeros. (The
+          // other slot may write the same zeros while this one's product reads them.)
+          for (int j = clear + (lane >> 3); j < cols; j += 4)
+            for (int b = 0; b < L::kBoxes; ++b)
+              *reinterpret_cast<uint4*>(sm.v + stage * L::kKB + b * L::kBox + j * 128 + (lane & 7) * 16) =
+                  make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
         if (!mbar_sleep_warp(&sm.p_full[i], mine & 1, guard)) return false;
-        if ((i ? t.uses1(x + 1) : t.uses0(x + 1)) && !wait_count(&sm.s_issued[i], mine + 2, guard)) return false;
+        if (!ends && !wait_count(&sm.s_issued[i], mine + 2, guard)) return false;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          if (kk * 16 < cols) umma_ts_one(one, d, pa + kk * 8, vd + kk * (2048 / 16), IDESC_O, (adds || kk > 0));
+          if (kk * 16 < cols) umma_ts_one(one, d, pa + kk * 8, vd + kk * (2048 / 16), IDESC_O, (r > 0 || kk > 0));
         umma_commit_one(one, &sm.pv_done[i]);
-        if (i == 1 || !u1) umma_commit_one(one, &sm.v_empty[stage]);
-        if (i) {
+        if (frees) umma_commit_one(one, &sm.v_empty[stage]);
+        if (i)
           ++n1;
-          begun1 = true;
-        } else {
+        else
           ++n0;
-          begun0 = true;
-        }
-      }
-      if (++stage == L::kStagesV) {
-        stage = 0;
-        par ^= 1;
       }
     }
+    tile0 += t.count;
   }
 }
 
@@ -563,8 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // P V of the tile before must be complete before O is rescaled or P overwritten (asked for here,
         // needed below)
         const bool pv_ok = n_s == 0 || mbar_test(&pv_done[slot], (n_s - 1) & 1);
-        // 32-column chunks that some row of the warp sees (the others cost nothing below)
-        uint32_t live = 15u;
+        // halves of the tile that some row of the warp sees (the others cost nothing below)
+        uint32_t live = 3u;
         if (__any_sync(0xffffffffu, x < first || base < key_lo || base + kKeys > key_hi)) {
           // a tile of first positions ends at the last of them; where the tiles run on from position 0
           // the first positions add to the window's
@@ -576,20 +586,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int at = base + 32 * c;
             const uint32_t seen = early ? bits_between(0, args.sinks - at)
                                         : bits_between(key_lo - at, key_hi - at) | bits_between(0, min(extra, key_hi) - at);
-            if (__any_sync(0xffffffffu, seen != 0)) {
-              live |= 1u << c;
-              if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
+            if (__any_sync(0xffffffffu, seen != 0)) live |= 1u << (c >> 1);
+            if (__any_sync(0xffffffffu, seen != 0xffffffffu)) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (!((seen >> i) & 1u)) r[c][i] = 0xff800000u;  // -inf
-              }
+              for (int i = 0; i < 32; ++i)
+                if (!((seen >> i) & 1u)) r[c][i] = 0xff800000u;  // -inf
             }
           }
         }
         float mx = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if ((live >> c) & 1u) mx = fmaxf(mx, max32(r[c]));
+        for (int h = 0; h < 2; ++h)
+          if ((live >> h) & 1u) mx = fmaxf(mx, fmaxf(max32(r[2 * h]), max32(r[2 * h + 1])));
         mx *= sl2;
         float alpha = 1.f;
         bool rescale = false;
@@ -602,22 +610,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float m_use = m_ref == -INFINITY ? 0.f : m_ref;  // a row with no key seen yet
         const uint64_t sl2_2 = f2_pack(sl2, sl2), negm_2 = f2_pack(-m_use, -m_use);
-        uint64_t sum2[4];
+        uint64_t sum2[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          sum2[c] = 0;
-          if ((live >> c) & 1u) {
+        for (int h = 0; h < 2; ++h) {
+          if ((live >> h) & 1u) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float x0, x1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1])), sl2_2, negm_2), x0, x1);
-              const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
-              sum2[c] = i == 0 ? f2_pack(e0, e1) : f2_add(sum2[c], f2_pack(e0, e1));
-              r[c >> 1][(c & 1) * 16 + (i >> 1)] = pack_bf16x2(e0, e1);
+            for (int c = 2 * h; c < 2 * h + 2; ++c) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                float x0, x1;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(r[c][i]), __uint_as_float(r[c][i + 1])), sl2_2, negm_2), x0,
+                          x1);
+                const float e0 = fast_exp2(x0), e1 = fast_exp2(x1);
+                sum2[c] = i == 0 ? f2_pack(e0, e1) : f2_add(sum2[c], f2_pack(e0, e1));
+                r[h][(c & 1) * 16 + (i >> 1)] = pack_bf16x2(e0, e1);
+              }
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) r[c >> 1][(c & 1) * 16 + i] = 0;
+            for (int i = 0; i < 32; ++i) r[h][i] = 0;
           }
         }
         if (!__all_sync(0xffffffffu, pv_ok) && !(ok = mbar_sleep_warp(&pv_done[slot], (n_s - 1) & 1, guard))) break;
