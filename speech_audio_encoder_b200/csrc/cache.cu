@@ -190,19 +190,21 @@ __global__ void __launch_bounds__(kPlanThreads, 1) resize_kernel(const PlanArgs 
     }
   }
   __syncthreads();
-  // what each entry asks for, and where its share of the free pages begins
+  // what each entry asks for, and where its share of the free pages begins (more than there are pages
+  // counts as one more, so that the sums of any list stay in 32 bits)
   int asked = 0;
   for (int base = 0; base < a.n; base += kPlanThreads) {
     const int i = base + tid;
     int need = 0, from;
     if (i < a.n) {
       const Entry e = entry_of(a, i);
-      need = pages_of(e.len, t.page_shift) - pages_of(e.kept, t.page_shift) + replaces(a, e, multi, from);
+      need = min(pages_of(e.len, t.page_shift) - pages_of(e.kept, t.page_shift) + replaces(a, e, multi, from),
+                 t.pages + 1);
     }
     int total;
     const int at = asked + block_scan(need, warp_sums, total);
     if (i < a.n) *SAL_CK_ST(a.offs + i, 4) = at;
-    asked += total;
+    asked = min(asked + total, t.pages + 1);
   }
   const int chunk = (words + kPlanThreads - 1) / kPlanThreads;
   const int w0 = min(words, tid * chunk), w1 = min(words, w0 + chunk);

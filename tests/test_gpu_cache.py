@@ -284,6 +284,22 @@ def test_the_largest_tables():
     assert torch.equal(c.table[1::2, :16][low], stay[low])
 
 
+def test_a_list_that_asks_for_more_than_32_bits_of_pages():
+    """64 sequences that each ask for 2^25 pages: 2^31 in all, of the 40 there are."""
+    api = _api()
+    c = api.PagedCache.empty(1, 40, 1, 8, 64, 65, 1 << 25)
+    api.sal_cache_resize(c, _ints([64]), _ints([20]))
+    c.check()
+    for n in (63, 64):
+        api.sal_cache_resize(c, _ints(range(n)), _ints([1 << 28] * n))
+        assert int(c.status.item()) == api.CACHE_NO_PAGES
+        c.status.zero_()
+        assert c.lengths.tolist() == [0] * 64 + [20] and c.table[64, :4].tolist() == [0, 1, 2, -1]
+        assert int(c.table[0].max()) == -1
+    del c
+    torch.cuda.empty_cache()
+
+
 def test_pages_past_32_bits():
     """A pool of 2.7 G elements: pages in its last gigabyte are written, copied and moved."""
     api = _api()
