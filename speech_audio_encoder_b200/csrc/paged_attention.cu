@@ -136,7 +136,8 @@ __device__ __forceinline__ void walk(const PagedArgs& a, const Span& sp, int seq
 #pragma unroll
       for (int i = 0; i < kIts; ++i) {
         const int r = row_in + (32 / C) * i;  // rows 0..7 in the first half of the copies
-        const bool fill = base + r < sp.n && (i < kIts / 2 ? e0 : e1) >= 0;
+        const int pos = base + r;
+        const bool fill = pos < sp.n && (pos >= sp.low || pos < sp.sinks) && (i < kIts / 2 ? e0 : e1) >= 0;
         const int64_t at = ((i < kIts / 2 ? at0 : at1 - 8) + r) * HD + chunk * 8;
         const uint32_t to = dst + r * R::kRow + ((chunk ^ (r & 7)) << 4);
         cp_async16(to, fill ? SAL_CK_LD(a.k + at, 16) : a.k, fill);

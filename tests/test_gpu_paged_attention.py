@@ -85,6 +85,22 @@ def test_pages_let_go_bad_entries_and_lengths():
     _compare(o, q, cache, 0, 90, 20)
 
 
+@pytest.mark.parametrize("H,kvh,d,page,left,sinks", [(10, 10, 128, 16, 100, 5), (16, 2, 64, 8, 37, 0), (4, 4, 128, 64, 0, 17)])
+def test_hidden_keys_and_values_that_are_no_numbers(H, kvh, d, page, left, sinks):
+    """Positions between the first ones and the window hold NaN and infinities, up to the visible
+    ones' edges: nothing of it reaches a result."""
+    lengths = [150, 333, 1000, 2 + left, left + sinks + 9]
+    cache, q = _make(lengths, H, kvh, d, page, seed=12)
+    clean = _api().sal_attention_paged(q, cache, left, sinks, 1)
+    for s, n in enumerate(lengths):
+        for j in range(sinks, n - 1 - left):
+            at = int(cache.table[s, j // page])
+            cache.k[:, at, :, j % page] = float("inf")
+            cache.v[:, at, :, j % page] = float("nan") if j % 2 else float("-inf")
+    assert torch.equal(_api().sal_attention_paged(q, cache, left, sinks, 1), clean)
+    _compare(clean, q, cache, 1, left, sinks)
+
+
 def test_rows_name_their_sequences():
     """Rows in another order, one sequence twice, sequences out of range (zeros)."""
     cache, _ = _make([40, 0, 333, 100], 10, 10, 128, 16, seed=2)
