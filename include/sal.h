@@ -461,8 +461,8 @@ sal_status sal_log_softmax(const float* z, int64_t rows, int n, int64_t ld, floa
  * when
  *     0 <= j < n   and   j <= p + right   and   (j >= p - left or j < sinks).
  * `sinks` first positions stay visible however far the window has moved. A negative left
- * or right is no limit. Keys and values at visible positions and at other positions of
- * [0, n) must be finite; what memory holds past n is never used.
+ * or right is no limit. What a key or value holds at a position that is not visible, infinite
+ * or not a number as it may be, does not reach p's result.
  * --------------------------------------------------------------------------------- */
 
 typedef struct {
@@ -511,8 +511,9 @@ sal_status sal_attention_window_withhold(const void* q, const void* k, const voi
  *               compact (may be NULL for the other calls)
  * page_size is a power of two in [8, 256], head_dim 64 or 128, pages at most
  * SAL_CACHE_MAX_PAGES, sequences at most SAL_CACHE_MAX_SEQUENCES, layers at most 32,767,
- * kv_heads at most 65,535, max_pages * page_size at most 2^28. Every call returns SAL_EINVAL for a null, misaligned (16 bytes; table,
- * lengths, status: 4) or negative member and SAL_ESHAPE for one out of these ranges. */
+ * kv_heads at most 65,535, max_pages * page_size at most 2^28. Every call returns SAL_EINVAL
+ * for a null, misaligned (16 bytes; table, lengths, status: 4) or negative member and
+ * SAL_ESHAPE for one out of these ranges. */
 typedef struct {
   void *k, *v;
   int layers, pages, kv_heads, page_size, head_dim;
@@ -528,10 +529,10 @@ size_t sal_cache_workspace_bytes(int pages, int sequences);
 
 /* Writes new keys and values into a layer's pages: token t of row b, k and v [batch,
  * kv_heads, T, head_dim] bf16, goes to position starts[b] + t (starts NULL: t) of sequence
- * seqs[b] (NULL: b). Tokens at positions outside [0, lengths[seq]), or whose page has been let go, and
- * rows with a sequence out of range, are skipped: so a row may bring fewer than T tokens,
- * and one whose sal_cache_resize failed writes nothing. Two tokens for one position (a
- * sequence named twice, or a page that two rows share) leave one of them there. */
+ * seqs[b] (NULL: b). Tokens at positions outside [0, lengths[seq]), or whose page has been
+ * let go, and rows with a sequence out of range, are skipped: so a row may bring fewer than
+ * T tokens, and one whose sal_cache_resize failed writes nothing. Two tokens for one
+ * position (a sequence named twice, or a page that two rows share) leave one of them there. */
 sal_status sal_cache_append(const sal_cache* cache, int layer, const void* k, const void* v, int batch, int64_t T,
                             const int32_t* starts, const int32_t* seqs, void* stream);
 

@@ -66,6 +66,7 @@ constexpr int kItems = 4;  // work items published ahead
 enum Pairing { kSingles, kTilePairs, kHeadPairs };
 
 struct WindowArgs {
+  const __nv_bfloat16 *q, *k, *v;
   __nv_bfloat16* o;
   const int32_t* lengths;
   int batch, T, heads, kv_heads;
@@ -184,6 +185,60 @@ __device__ __forceinline__ bool wait_count(volatile uint32_t* count, uint32_t ne
     if (__any_sync(0xffffffffu, *g.abort != 0 || now - t0 > g.limit_ns)) return false;
   }
   return true;
+}
+
+// Eight bf16 values as fp32.
+__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+// One row by a warp, straight from memory: row qi of q over the keys [0, lo) and [mid, hi) of the plane
+// of keys that begins at row ki, with the maximum and the sum of weights that are known. 32 keys at a
+// time, a score to a lane; then every lane adds up its columns.
+template <int HD>
+__device__ __forceinline__ void sum_again(const WindowArgs& a, int64_t qi, int64_t ki, int lo, int mid, int hi, float m,
+                                          float inv_l, __nv_bfloat16* dst) {
+  constexpr int kCols = HD / 32;
+  const int lane = threadIdx.x & 31, count = lo + max(0, hi - mid);
+  float o[kCols] = {};
+#pragma unroll 1
+  for (int t0 = 0; t0 < count; t0 += 32) {
+    const int t = min(t0 + lane, count - 1), j = t < lo ? t : mid + t - lo, n = min(32, count - t0);
+    float s = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < HD; d += 8) {
+      float x[8], y[8];
+      unpack8(*SAL_CK_LD(reinterpret_cast<const uint4*>(a.q + qi * HD + d), 16), x);
+      unpack8(*SAL_CK_LD(reinterpret_cast<const uint4*>(a.k + (ki + j) * HD + d), 16), y);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s = fmaf(x[i], y[i], s);
+    }
+    const float w = fast_exp2(fmaf(s, a.scale_log2, -m));
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const int ji = __shfl_sync(0xffffffffu, j, i);
+#pragma unroll
+      for (int e = 0; e < kCols; e += 2) {
+        const uint32_t y =
+            *SAL_CK_LD(reinterpret_cast<const uint32_t*>(a.v + (ki + ji) * HD + lane * kCols + e), 4);
+        o[e] = fmaf(wi, __uint_as_float(y << 16), o[e]);
+        o[e + 1] = fmaf(wi, __uint_as_float(y & 0xffff0000u), o[e + 1]);
+      }
+    }
+    bool lost = true;  // no numbers any more, and so they stay
+#pragma unroll
+    for (int e = 0; e < kCols; ++e) lost = lost && o[e] != o[e];
+    if (__all_sync(0xffffffffu, lost)) break;
+  }
+#pragma unroll
+  for (int e = 0; e < kCols; e += 2)
+    *SAL_CK_ST(reinterpret_cast<uint32_t*>(dst + lane * kCols + e), 4) = pack_bf16x2(o[e] * inv_l, o[e + 1] * inv_l);
 }
 
 // Where everything is in shared memory.
@@ -658,19 +713,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       const bool stored = p < it.n;
-      __nv_bfloat16* dst = args.o + ((static_cast<int64_t>(it.b) * args.T + p) * args.heads + it.head[slot]) * HD;
+      const int head = it.head[slot], b = it.b, kv = it.kv;
+      __nv_bfloat16* dst = args.o + ((static_cast<int64_t>(b) * args.T + p) * args.heads + head) * HD;
       __syncwarp();
       if (lane == 0) done_with(k);
       if (!begun) continue;  // an empty slot
       if (!(ok = mbar_sleep_warp(&pv_done[slot], (n_s - 1) & 1, guard))) break;
       tc_fence_after();
       const float inv_l = 1.0f / l;
+      uint64_t zeros[4] = {0, 0, 0, 0};  // zero times every value of the row
 #pragma unroll 1
       for (int c = 0; c < HD / 64; ++c) {
         uint32_t u[2][32];
         tmem_ld32(colO + 64 * c, u[0]);
         tmem_ld32(colO + 64 * c + 32, u[1]);
         tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 64; i += 2) {
+          uint64_t& z = zeros[(i >> 1) & 3];
+          z = f2_fma(f2_pack(__uint_as_float(u[i >> 5][i & 31]), __uint_as_float(u[i >> 5][(i & 31) + 1])), 0, z);
+        }
         if (stored) {
 #pragma unroll
           for (int i = 0; i < 32; ++i)
@@ -686,6 +748,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                   make_uint4(u[0][4 * i], u[0][4 * i + 1], u[0][4 * i + 2], u[0][4 * i + 3]);
           }
         }
+      }
+      float zero_lo, zero_hi;
+      f2_unpack(f2_add(f2_add(zeros[0], zeros[1]), f2_add(zeros[2], zeros[3])), zero_lo, zero_hi);
+      // A value that is no number, at a key of these tiles that the row need not see, has met a weight
+      // of zero: such a row is summed again over what it does see.
+      uint32_t again = __ballot_sync(0xffffffffu, stored && !(zero_lo + zero_hi == 0.f));
+#pragma unroll 1
+      for (; again; again &= again - 1) {
+        const int r = __ffs(again) - 1;
+        auto of = [&](auto x) { return __shfl_sync(0xffffffffu, x, r); };
+        const int lo = of(key_lo), hi = of(key_hi);
+        const int64_t at = of(p);
+        __syncwarp();  // the row's own stores are behind these
+        sum_again<HD>(args, (static_cast<int64_t>(b) * args.heads + head) * args.T + at, static_cast<int64_t>(kv) * args.T,
+                      min(args.sinks, min(lo, hi)), lo, hi, of(m_ref == -INFINITY ? 0.f : m_ref), of(inv_l),
+                      args.o + ((static_cast<int64_t>(b) * args.T + at) * args.heads + head) * HD);
       }
       // (O is overwritten by the next item's first product, which waits for this slot's next P)
     }
@@ -746,6 +824,9 @@ sal_status window_attention_launch(const void* q, const void* k, const void* v, 
   const int sms = ready_sms();
   if (!sms) return SAL_ECUDA;
   WindowArgs a{};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lengths = lengths;
   a.batch = batch;
@@ -781,6 +862,9 @@ sal_status window_attention_launch(const void* q, const void* k, const void* v, 
       !make_tmap_3d_bf16(&tk, k, hd, rows, kvp, 64, kKeys, 1) ||
       !make_tmap_3d_bf16(&tv, v, hd, rows, kvp, 64, kKeys, 1))
     return SAL_ECUDA;
+  ck_declare(q, static_cast<uint64_t>(planes) * rows * hd * 2, false);
+  ck_declare(k, kvp * rows * hd * 2, false);
+  ck_declare(v, kvp * rows * hd * 2, false);
   ck_declare(o, static_cast<uint64_t>(planes) * rows * hd * 2, true);
   ck_declare(lengths, static_cast<uint64_t>(batch) * 4, false);
   const dim3 grid(static_cast<unsigned>(std::min(sms, a.items)));

@@ -4,7 +4,7 @@ lengths, what lies past them, other streams, captured graphs, offsets past 32 bi
 import pytest
 import torch
 
-from stream_ref import attention_bound, window_reference
+from stream_ref import attention_bound, visible, window_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -84,6 +84,28 @@ def test_lengths_and_what_lies_past_them(T, H, kvh, d, left, right, sinks):
     for b in (3, 4, 5):
         alone = [x[b:b + 1, :, :lens[b]].contiguous() for x in clean]
         _compare(api.sal_attention_window(*alone, left=left, right=right, sinks=sinks), *alone, left, right, sinks)
+
+
+@pytest.mark.parametrize("T,H,kvh,d,left,right,sinks", [
+    (300, 2, 2, 128, 20, 0, 4), (300, 4, 2, 64, 40, 10, 0), (1500, 10, 10, 128, 100, 0, 200), (3000, 16, 16, 64, 33, 65, 3),
+    (2100, 8, 2, 128, 150, 0, 4), (200, 3, 3, 128, -1, 0, 0)])
+def test_values_that_are_no_numbers(T, H, kvh, d, left, right, sinks):
+    """Keys and values that are infinite or NaN reach the rows that see them, and no other row of
+    their tiles."""
+    q, k, v = _inputs(2, T, H, kvh, d, seed=11)
+    wrong = torch.zeros(T, dtype=torch.bool)
+    for at, (x, bad) in zip((T // 7, T // 2, T // 2 + 70, T - 5),
+                            ((v, float("nan")), (v, float("-inf")), (k, float("nan")), (v, float("inf")))):
+        x[0, :, at] = bad
+        wrong[at] = True
+    o = _api().sal_attention_window(q, k, v, left=left, right=right, sinks=sinks).double().reshape(2, T, H, d)
+    p = torch.arange(T)[:, None]
+    hit = (visible(p, torch.arange(T)[None, :], T, left, right, sinks) & wrong[None, :]).any(1).cuda()
+    assert 0 < int(hit.sum()) < T
+    ref, spread = window_reference(q, k, v, left, right, sinks, [T, T])
+    off = (o - ref).abs() - attention_bound(ref, spread)
+    assert bool((off[0, ~hit] <= 0).all()) and bool((off[1] <= 0).all())
+    assert not bool(torch.isfinite(o[0, hit]).any())
 
 
 @pytest.mark.parametrize("d", [64, 128])
