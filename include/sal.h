@@ -462,7 +462,8 @@ sal_status sal_log_softmax(const float* z, int64_t rows, int n, int64_t ld, floa
  *     0 <= j < n   and   j <= p + right   and   (j >= p - left or j < sinks).
  * `sinks` first positions stay visible however far the window has moved. A negative left
  * or right is no limit. What a key or value holds at a position that is not visible, infinite
- * or not a number as it may be, does not reach p's result.
+ * or not a number as it may be, does not reach p's result. The first of these calls on a
+ * device sets its kernels up; make it before any stream capture.
  * --------------------------------------------------------------------------------- */
 
 typedef struct {

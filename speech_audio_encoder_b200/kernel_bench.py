@@ -4,7 +4,8 @@
 
 KIND is one of frontend, stack_proj, layernorm, qkv, attention, out_proj, ffn_up, ffn_down,
 speaker_fuse, connector, ctc (the whole CTC adapter), attention64 (its 16 heads of 64),
-linear (any --N, --K, --epi).
+window and paged (attention with --left, --right and --sinks over clips of T positions, and of
+one position over a paged cache of T; --heads, --kv-heads, --head-dim), linear (any --N, --K, --epi).
 Each repetition is one launch (qkv also launches the small RoPE-table kernel). The
 repetitions are captured once as a CUDA graph and the replay is timed with CUDA events on
 the launching stream after warm-up (eager launches from Python would measure the host). Prints one JSON line with the
@@ -37,6 +38,13 @@ def main():
     ap.add_argument("--N", type=int, default=1280, help="linear: output width")
     ap.add_argument("--K", type=int, default=1280, help="linear: reduction length")
     ap.add_argument("--epi", type=int, default=1, help="linear: sal_epilogue value")
+    ap.add_argument("--heads", type=int, default=10, help="window, paged: query heads")
+    ap.add_argument("--kv-heads", type=int, default=10, help="window, paged: key/value heads")
+    ap.add_argument("--head-dim", type=int, default=128, help="window, paged: 64 or 128")
+    ap.add_argument("--left", type=int, default=-1, help="window, paged: visible positions before (-1: all)")
+    ap.add_argument("--right", type=int, default=0, help="window: visible positions after (-1: all)")
+    ap.add_argument("--sinks", type=int, default=0, help="window, paged: first positions that stay visible")
+    ap.add_argument("--page", type=int, default=16, help="paged: positions of a page")
     a = ap.parse_args()
     B, T = a.batch, a.T
     M = B * T
@@ -77,6 +85,29 @@ def main():
 
         def run():
             api.sal_attention_heads(q, k, v)
+    elif a.kind == "window":
+        q, k, v = (_bf16((B, h, T, a.head_dim), 30 + i, 1.0) for i, h in enumerate((a.heads, a.kv_heads, a.kv_heads)))
+        p = np.arange(T)
+        lo = np.maximum(0, p - a.left) if a.left >= 0 else np.zeros(T, dtype=np.int64)
+        hi = np.minimum(T, p + a.right + 1) if a.right >= 0 else np.full(T, T)
+        flops = 4.0 * B * a.heads * a.head_dim * float((hi - lo + np.minimum(a.sinks, lo)).sum())
+        out = torch.empty((M, a.heads * a.head_dim), dtype=torch.bfloat16, device="cuda")
+
+        def run():
+            api.sal_attention_window(q, k, v, a.left, a.right, a.sinks, out=out)
+    elif a.kind == "paged":
+        per = -(-T // a.page)
+        order = torch.from_numpy(np.random.default_rng(0).permutation(B * per).astype(np.int32)).cuda()
+        k, v = (torch.randn((1, B * per, a.kv_heads, a.page, a.head_dim), device="cuda").bfloat16() for _ in range(2))
+        cache = api.PagedCache(k, v, order.reshape(B, per), torch.full((B,), T, dtype=torch.int32, device="cuda"))
+        q = torch.randn((B, a.heads, a.head_dim), device="cuda").bfloat16()
+        out = torch.empty((B, a.heads * a.head_dim), dtype=torch.bfloat16, device="cuda")
+        ws = api.attention_paged_workspace(cache, B, a.heads)
+        low = max(0, T - 1 - a.left) if a.left >= 0 else 0
+        bytes_ = 4.0 * B * a.kv_heads * a.head_dim * (T - low + min(a.sinks, low))
+
+        def run():
+            api.sal_attention_paged(q, cache, a.left, a.sinks, out=out, workspace=ws)
     elif a.kind == "speaker_fuse":
         H = _bf16((M, 1280), 7, 1.0)
         P = torch.from_numpy(synth.speaker_activity(M, 1)).cuda()
