@@ -109,21 +109,69 @@ struct Item {
   __device__ int base(int x) const { return x < first ? kKeys * x : start + kKeys * (x - first); }
 };
 
-__device__ __forceinline__ Item item_of(const WindowArgs& a, int idx) {
-  Item it;
-  // the rows of the longest reach (a causal clip's last tiles) come first
-  int h, t0;
-  if (a.pairing == kHeadPairs) {
-    const int planes = a.batch * (a.heads >> 1), pl = idx % planes;
-    it.b = pl / (a.heads >> 1);
-    h = 2 * (pl % (a.heads >> 1));
-    t0 = a.tiles - 1 - idx / planes;
-  } else {
-    const int planes = a.batch * a.heads, pl = idx % planes;
-    it.b = pl / a.heads;
-    h = pl % a.heads;
-    t0 = a.pairing == kTilePairs ? 2 * ((a.tiles + 1) / 2 - 1 - idx / planes) : a.tiles - 1 - idx / planes;
+// The items of a call in the order of their numbers: those of the longest reach (a causal clip's last
+// tiles) first, without those past a clip's end, so that clips of different lengths leave every block
+// as many. A whole warp asks for ever higher numbers.
+struct Items {
+  int rows, per;             // rows of items (one, or a pair, of query tiles each), items of a clip in a row
+  int r = 0, before = 0;     // the row it is at, items before it
+  int clips, held = 0;       // clips that reach into it (-1: not counted yet); a lane's length where all fit
+
+  __device__ __forceinline__ explicit Items(const WindowArgs& a)
+      : rows(a.pairing == kTilePairs ? (a.tiles + 1) / 2 : a.tiles),
+        per(a.pairing == kHeadPairs ? a.heads >> 1 : a.heads),
+        clips(-1) {
+    if (!a.lengths) return;
+    int most = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) most = max(most, held = length(a, b0 + (threadIdx.x & 31)));
+    most = __reduce_max_sync(0xffffffffu, most);
+    r = rows - (most + tile_rows(a) - 1) / tile_rows(a);  // nobody reaches the rows before
   }
+  __device__ __forceinline__ static int tile_rows(const WindowArgs& a) { return a.pairing == kTilePairs ? 2 * kTile : kTile; }
+  __device__ __forceinline__ static int length(const WindowArgs& a, int b) {
+    return b < a.batch ? min(max(*SAL_CK_LD(a.lengths + b, 4), 0), a.T) : 0;
+  }
+  // the clips b0 + i that reach into row r
+  __device__ __forceinline__ uint32_t reach(const WindowArgs& a, int b0) const {
+    const int n = a.batch <= 32 ? held : length(a, b0 + (threadIdx.x & 31));
+    return __ballot_sync(0xffffffffu, n > (rows - 1 - r) * tile_rows(a));
+  }
+  // clip, (first) head and (first) query tile of item j; false behind the last
+  __device__ __forceinline__ bool find(const WindowArgs& a, int j, int& b, int& h, int& tile) {
+    if (!a.lengths) {
+      r = j / (a.batch * per);
+      before = r * a.batch * per;
+    }
+    for (;; ++r, before += clips * per, clips = -1) {
+      if (r >= rows) return false;
+      if (clips < 0) {
+        clips = a.lengths ? 0 : a.batch;
+        for (int b0 = 0; a.lengths && b0 < a.batch; b0 += 32) clips += __popc(reach(a, b0));
+      }
+      if (j < before + clips * per) break;
+    }
+    int rank = (j - before) / per;
+    h = (j - before) - rank * per;
+    b = rank;
+    for (int b0 = 0; a.lengths; b0 += 32) {
+      uint32_t in = reach(a, b0);
+      const int n = __popc(in);
+      if (rank < n) {
+        for (; rank > 0; --rank) in &= in - 1;
+        b = b0 + __ffs(in) - 1;
+        break;
+      }
+      rank -= n;
+    }
+    h = a.pairing == kHeadPairs ? 2 * h : h;
+    tile = (rows - 1 - r) * (tile_rows(a) / kTile);
+    return true;
+  }
+};
+
+__device__ __forceinline__ Item item_of(const WindowArgs& a, int b, int h, int t0) {
+  Item it;
+  it.b = b;
   it.n = a.T;
   if (a.lengths) it.n = min(max(*SAL_CK_LD(a.lengths + it.b, 4), 0), a.T);
   it.kv = it.b * a.kv_heads + h / (a.heads / a.kv_heads);
@@ -570,28 +618,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     drain_products(&sm.drains[1], issue_outputs<HD>(args, sm, guard, tmem), guard);
   } else if (warp == 3) {
     if (args.lengths) pdl_wait();
-    if (lane == 0) {
-      // works the items out one ahead of the other roles (those past a clip's end are left out, an
-      // item of no tiles is the end), and loads the values: a thread of its own, so that a key tile
-      // never waits for a value tile's place
-      int idx = blockIdx.x, nth[2] = {0, 0};
-      Item now, next;
-      for (int k = -1; ok; ++k) {
+    // works the items out one ahead of the other roles (an item of no tiles is the end), and loads the
+    // values: a thread of its own, so that a key tile never waits for a value tile's place
+    Items list(args);
+    int idx = blockIdx.x, nth[2] = {0, 0};
+    Item now, next;
+    for (int k = -1; __shfl_sync(0xffffffffu, ok, 0); ++k) {
+      int b, h, t0;
+      const bool more = list.find(args, idx, b, h, t0);
+      idx += gridDim.x;
+      if (lane == 0) {
         next.count = 0;
-        for (; idx < args.items; idx += gridDim.x) {
-          next = item_of(args, idx);
-          if (next.count > 0) break;
-        }
-        idx += gridDim.x;
+        if (more) next = item_of(args, b, h, t0);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           next.nth[i] = nth[i];
           nth[i] += next.count > 0 && next.hi[i] > 0;
         }
         const int at = (k + 1) % kItems;
-        if (!(ok = mbar_sleep(&item_empty[at], (((k + 1) / kItems) & 1) ^ 1, guard))) break;
-        items[at] = next;
-        mbar_arrive(&item_full[at]);
+        if ((ok = mbar_sleep(&item_empty[at], (((k + 1) / kItems) & 1) ^ 1, guard))) {
+          items[at] = next;
+          mbar_arrive(&item_full[at]);
+        }
         if (k < 0) pdl_wait();
         if (k >= 0) {
           for (int x = 0; ok && x < now.count; ++x) {
@@ -604,8 +652,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         now = next;
-        if (now.count == 0) break;
       }
+      if (!more) break;
     }
   }
   } else {
