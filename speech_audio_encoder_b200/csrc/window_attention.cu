@@ -621,12 +621,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // works the items out one ahead of the other roles (an item of no tiles is the end), and loads the
     // values: a thread of its own, so that a key tile never waits for a value tile's place
     Items list(args);
-    int idx = blockIdx.x, nth[2] = {0, 0};
+    int nth[2] = {0, 0};
     Item now, next;
     for (int k = -1; __shfl_sync(0xffffffffu, ok, 0); ++k) {
       int b, h, t0;
-      const bool more = list.find(args, idx, b, h, t0);
-      idx += gridDim.x;
+      // to and fro over the blocks, so that no block gets the longest of every round
+      const int round = k + 1, at_block = round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+      const bool more = list.find(args, round * static_cast<int>(gridDim.x) + at_block, b, h, t0);
       if (lane == 0) {
         next.count = 0;
         if (more) next = item_of(args, b, h, t0);
