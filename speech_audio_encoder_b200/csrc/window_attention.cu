@@ -28,8 +28,8 @@
 //
 // Measured on one B200, inputs larger than L2: an hour (44,999 positions, 10 heads of 128, 750 back
 // and 8 first positions) 259-270 us, 0.65-0.67 PFLOP/s, 40 % of what a large library product reaches
-// here; 2 x 8,191 positions with 32 heads on 2, 1,023 back, 217 us (0.72 PFLOP/s); head dim
-// 64, 44,998 x 16, 250 on either side 228 us; 16 clips of up to a minute 44 us; 374 positions 7.6 us.
+// here; 2 x up to 8,191 positions with 32 heads on 2, 1,023 back, 201 us (0.77 PFLOP/s); head dim
+// 64, 44,998 x 16, 250 on either side 229 us; 16 clips of up to a minute 36 us; 374 positions 7.8 us.
 // What bounds it is the softmax's chain: S into registers, maximum, exponentials, P back, with two
 // warps per scheduler to hide its latencies; counters of the hour: tensor pipe 41 %, exp2 unit 44 %,
 // issue 43 %. A pair of tiles takes about 4,000 clocks, of which the products are 2,080.
@@ -37,7 +37,8 @@
 // scores it was made from 428 / 333 / 369; 64-key tiles with an issuer per slot 308 / 263 / 252; sixteen softmax
 // warps on half rows each 362 / 267 / 282; one issuing warp 326 / 306 / 281; a copy of the
 // loop without masks for whole tiles 312 / 308 / 237 (instruction fetch); 3 in 16 exponentials on the
-// FMA pipe 278 / 233 / 218.
+// FMA pipe 278 / 233 / 218. Items taken in turn with the padded ones among them, 16 clips of up to a
+// minute 44 us (36); first positions and the window's first keys in one tile 282 / 242 / 208 (268 / 232 / 201).
 #define SAL_CK_FILE 6
 #include <cuda_bf16.h>
 #include <math.h>
