@@ -86,6 +86,30 @@ def test_lengths_and_what_lies_past_them(T, H, kvh, d, left, right, sinks):
         _compare(api.sal_attention_window(*alone, left=left, right=right, sinks=sinks), *alone, left, right, sinks)
 
 
+@pytest.mark.parametrize("B,T,H,kvh,d", [(33, 300, 2, 2, 128), (70, 257, 4, 2, 64), (64, 129, 3, 3, 64),
+                                         (100, 40, 4, 4, 128), (2, 4000, 10, 10, 128)])
+@pytest.mark.parametrize("which", ["ragged", "one", "none"])
+def test_many_clips_of_different_lengths(B, T, H, kvh, d, which):
+    """The list of items that lengths reach: more clips than a warp has lanes, most of them short,
+    one alone, none at all."""
+    g = torch.Generator().manual_seed(B + T)
+    lens = torch.randint(0, T + 1, (B,), generator=g)
+    lens[torch.rand(B, generator=g) < 0.4] = 0
+    lens[B // 2] = T
+    if which != "ragged":
+        lens[torch.arange(B) != B // 2] = 0
+    if which == "none":
+        lens[:] = 0
+    lens = lens.tolist()
+    q, k, v = _inputs(B, T, H, kvh, d, seed=13)
+    o = torch.full((B * T, H * d), 7.0, dtype=torch.bfloat16, device="cuda")
+    _api().sal_attention_window(q, k, v, left=90, right=5, sinks=2,
+                                lengths=torch.tensor(lens, dtype=torch.int32, device="cuda"), out=o)
+    _compare(o, q, k, v, 90, 5, 2, lens)
+    rows = o.reshape(B, T, H * d)
+    assert all(bool((rows[b, n:] == 7.0).all()) for b, n in enumerate(lens))
+
+
 @pytest.mark.parametrize("T,H,kvh,d,left,right,sinks", [
     (300, 2, 2, 128, 20, 0, 4), (300, 4, 2, 64, 40, 10, 0), (1500, 10, 10, 128, 100, 0, 200), (3000, 16, 16, 64, 33, 65, 3),
     (2100, 8, 2, 128, 150, 0, 4), (200, 3, 3, 128, -1, 0, 0)])
