@@ -283,7 +283,7 @@ __device__ __forceinline__ void merge_weights(const uint8_t* smem, int rows, Mer
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const int at = w * kRowTile + r;
-      const float f = sml[2 * at + 1] > 0.f ? fast_exp2(sml[2 * at] - mm) : 0.f;
+      const float f = sml[2 * at + 1] != 0.f ? fast_exp2(sml[2 * at] - mm) : 0.f;
       total += sml[2 * at + 1] * f;
       m.weight[r][w] = f;
     }
@@ -308,10 +308,12 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return a / b;
 }
 
+// (A total of zero is a row that sees nothing. One that is no number, from a query, key or value
+// that is none, is stored as such, as the formula has it.)
 template <int HD>
 __device__ __forceinline__ void store_out(const PagedArgs& a, int b, int h, int d, float x, float total) {
   *SAL_CK_ST(a.o + (static_cast<int64_t>(b) * a.heads + h) * HD + d, 2) =
-      __float2bfloat16(total > 0.f ? x / total : 0.f);
+      __float2bfloat16(total == 0.f ? 0.f : x / total);
 }
 
 // Few keys: one cluster per (row, heads of a key head), its blocks each a split of the keys,
@@ -355,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_cluster_kernel(const PagedA
     for (int w = 0; w < a.splits; ++w) mm = fmaxf(mm, ld_cluster_f32(at, w));
     for (int w = 0; w < a.splits; ++w) {
       const float lw = ld_cluster_f32(at + 4, w);
-      const float f = lw > 0.f ? fast_exp2(ld_cluster_f32(at, w) - mm) : 0.f;
+      const float f = lw != 0.f ? fast_exp2(ld_cluster_f32(at, w) - mm) : 0.f;
       total += lw * f;
       x += ld_cluster_f32(xo, w) * f;
     }
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_line_kernel(const PagedArgs
 #pragma unroll 4
             for (int w = 0; w < pieces; ++w) {
               const float2 st = __ldcg(SAL_CK_LD(a.stats + place(w), 8));
-              const float f = st.y > 0.f ? fast_exp2(st.x - mm) : 0.f;
+              const float f = st.y != 0.f ? fast_exp2(st.x - mm) : 0.f;
               total += st.y * f;
               x += __ldcg(SAL_CK_LD(a.part + place(w) * HD + d, 4)) * f;
             }
@@ -539,7 +541,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArg
   for (int i = 0; i < kMine; ++i) {
     const int w = tid + i * kJoinThreads;
     if (w < n) {
-      weight[w] = st[i].y > 0.f ? fast_exp2(st[i].x - mm) : 0.f;
+      weight[w] = st[i].y != 0.f ? fast_exp2(st[i].x - mm) : 0.f;
       mine += st[i].y * weight[w];
     }
   }
