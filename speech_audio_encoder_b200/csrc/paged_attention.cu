@@ -43,6 +43,9 @@ constexpr int kRowTile = 16;             // query rows of a block: the heads tha
 constexpr int kClusterSplits = 8;        // splits that join inside a cluster
 constexpr int kSlots = 148 * 2;          // blocks that fit on the GPU at once
 constexpr int kFewKeys = 8;              // blocks of keys below which a split is not worth its start
+// The least maximum of a row that has seen a key: scores of -infinity are then weights of zero (minus
+// a maximum of -infinity they would be NaN), and a maximum of -infinity means that nothing is visible.
+constexpr float kLeastMax = -3.402823466e38f;
 
 template <int HD>
 struct Ring {
@@ -210,7 +213,7 @@ __device__ __forceinline__ void walk(const PagedArgs& a, const Span& sp, int seq
         float mx = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        mx *= a.scale_log2;
+        mx = fmaxf(mx * a.scale_log2, kLeastMax);
         fac[r] = 1.f;
         if (mx > m[r]) {
           fac[r] = fast_exp2(m[r] - mx);
@@ -283,7 +286,7 @@ __device__ __forceinline__ void merge_weights(const uint8_t* smem, int rows, Mer
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const int at = w * kRowTile + r;
-      const float f = sml[2 * at + 1] != 0.f ? fast_exp2(sml[2 * at] - mm) : 0.f;
+      const float f = sml[2 * at] != -INFINITY ? fast_exp2(sml[2 * at] - mm) : 0.f;
       total += sml[2 * at + 1] * f;
       m.weight[r][w] = f;
     }
@@ -308,12 +311,12 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return a / b;
 }
 
-// (A total of zero is a row that sees nothing. One that is no number, from a query, key or value
-// that is none, is stored as such, as the formula has it.)
+// A row that sees nothing (its maximum is -infinity) is zeros. A total that is no number, from a query,
+// key or value that is none, is stored as such, and so is 0 / 0 where every visible score is -infinity.
 template <int HD>
-__device__ __forceinline__ void store_out(const PagedArgs& a, int b, int h, int d, float x, float total) {
+__device__ __forceinline__ void store_out(const PagedArgs& a, int b, int h, int d, float x, float total, float top) {
   *SAL_CK_ST(a.o + (static_cast<int64_t>(b) * a.heads + h) * HD + d, 2) =
-      __float2bfloat16(total == 0.f ? 0.f : x / total);
+      __float2bfloat16(top == -INFINITY ? 0.f : x / total);
 }
 
 // Few keys: one cluster per (row, heads of a key head), its blocks each a split of the keys,
@@ -340,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_cluster_kernel(const PagedA
   for (int r = threadIdx.x / HD; r < rows; r += kThreads / HD) {
     const float x = merged<HD>(smem, mg, r, d), mm = mg.top[r], total = mg.total[r];
     if (a.splits == 1) {
-      store_out<HD>(a, b, h0 + r, d, x, total);
+      store_out<HD>(a, b, h0 + r, d, x, total, mm);
       continue;
     }
     so[r * R::kPitch + d] = x;  // this thread alone has read column d of row r
@@ -356,12 +359,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_cluster_kernel(const PagedA
     float mm = -INFINITY, x = 0.f, total = 0.f;
     for (int w = 0; w < a.splits; ++w) mm = fmaxf(mm, ld_cluster_f32(at, w));
     for (int w = 0; w < a.splits; ++w) {
-      const float lw = ld_cluster_f32(at + 4, w);
-      const float f = lw != 0.f ? fast_exp2(ld_cluster_f32(at, w) - mm) : 0.f;
-      total += lw * f;
+      const float mw = ld_cluster_f32(at, w), f = mw != -INFINITY ? fast_exp2(mw - mm) : 0.f;
+      total += ld_cluster_f32(at + 4, w) * f;
       x += ld_cluster_f32(xo, w) * f;
     }
-    store_out<HD>(a, b, h0 + r, d, x, total);
+    store_out<HD>(a, b, h0 + r, d, x, total, mm);
   }
   cluster_barrier();  // nobody's shared memory goes away while another block reads it
 }
@@ -461,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_line_kernel(const PagedArgs
       for (int r = tid / HD; r < rows; r += kThreads / HD) {
         const float x = merged<HD>(smem, mg, r, d), mm = mg.top[r], total = mg.total[r];
         if (whole) {
-          store_out<HD>(a, b, h0 + r, d, x, total);
+          store_out<HD>(a, b, h0 + r, d, x, total, mm);
           continue;
         }
         const int to = (2 * c + (lo == 0)) * kRowTile + r;
@@ -483,11 +485,11 @@ __global__ void __launch_bounds__(kThreads, 2) paged_line_kernel(const PagedArgs
 #pragma unroll 4
             for (int w = 0; w < pieces; ++w) {
               const float2 st = __ldcg(SAL_CK_LD(a.stats + place(w), 8));
-              const float f = st.y != 0.f ? fast_exp2(st.x - mm) : 0.f;
+              const float f = st.x != -INFINITY ? fast_exp2(st.x - mm) : 0.f;
               total += st.y * f;
               x += __ldcg(SAL_CK_LD(a.part + place(w) * HD + d, 4)) * f;
             }
-            store_out<HD>(a, b, h0 + r, d, x, total);
+            store_out<HD>(a, b, h0 + r, d, x, total, mm);
           }
           if (tid == 0) *SAL_CK_ST(a.arrived + from, 4) = 0;
         }
@@ -500,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_line_kernel(const PagedArgs
   // rows without keys have no part: zeros
   for (int b = c; b < a.batch; b += gridDim.x)
     if (span_of(a, seq_of(b)).blocks == 0) {
-      for (int i = tid; i < a.heads * HD; i += kThreads) store_out<HD>(a, b, 0, i, 0.f, 0.f);
+      for (int i = tid; i < a.heads * HD; i += kThreads) store_out<HD>(a, b, 0, i, 0.f, 0.f, -INFINITY);
       if (!a.by_part && !a.inside)
         for (int i = tid; i < groups; i += kThreads) *SAL_CK_ST(a.joins + b * groups + i, 16) = make_int4(0, 0, 0, 0);
     }
@@ -541,7 +543,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArg
   for (int i = 0; i < kMine; ++i) {
     const int w = tid + i * kJoinThreads;
     if (w < n) {
-      weight[w] = st[i].y != 0.f ? fast_exp2(st[i].x - mm) : 0.f;
+      weight[w] = st[i].x != -INFINITY ? fast_exp2(st[i].x - mm) : 0.f;
       mine += st[i].y * weight[w];
     }
   }
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedArg
     y += sums[i][tid];
     total += reduced[i];
   }
-  store_out<HD>(a, join.x, kvh * share + r0 + r, tid, y, total);
+  store_out<HD>(a, join.x, kvh * share + r0 + r, tid, y, total, mm);
 }
 
 // How a call runs: clusters of `splits` blocks, or (splits == 0) a line of `grid` parts.

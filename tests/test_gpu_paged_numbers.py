@@ -5,6 +5,8 @@ kernel."""
 import pytest
 import torch
 
+from stream_ref import attend, attention_bound
+
 pytestmark = pytest.mark.gpu
 
 # lengths, heads, kv_heads, head_dim, page: which way the call runs
@@ -87,3 +89,36 @@ def test_a_row_without_keys_is_zeros_beside_one_that_is_no_number(way):
     cache.lengths[1] = 0
     o = _api().sal_attention_paged(q, cache)
     assert bool(torch.isnan(o[0]).all()) and not bool(o[1].any()) and bool(torch.isfinite(o[2:]).all())
+
+
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("which", ["the last", "the first sixteen", "every other sixteen", "all but one", "all"])
+def test_scores_of_minus_infinity(way, which):
+    """Visible keys whose score is -infinity have a weight of zero, also where a block of sixteen, a
+    warp's or a piece's share of them has no other; where all of a row's are, the formula is 0 / 0."""
+    lengths, H, kvh, d, page = WAYS[way]
+    lengths = [lengths[0] + 1, *lengths[1:]]
+    while lengths[0] % 16 != 1:  # the last key is alone in its block
+        lengths[0] += 1
+    cache, q = _make(lengths, H, kvh, d, page)
+    clean = _api().sal_attention_paged(q, cache).reshape(len(lengths), H, d)
+    q[0, :, 5] = 1.0
+    n = lengths[0]
+    j = torch.arange(n)
+    off = {"the last": j == n - 1, "the first sixteen": j < 16, "every other sixteen": j // 16 % 2 == 0,
+           "all but one": j != n // 2, "all": j >= 0}[which]
+    at = torch.tensor([_place(cache, 0, x) for x in range(n)], device="cuda")
+    lost = at[off.cuda()]
+    cache.k[0, lost[:, 0], :, lost[:, 1], 5] = float("-inf")
+    o = _api().sal_attention_paged(q, cache).reshape(clean.shape)
+    assert torch.equal(o[1:], clean[1:])
+    if which == "all":
+        assert bool(torch.isnan(o[0]).all())
+        return
+    share = H // kvh
+    for h in range(kvh):
+        rows = slice(h * share, (h + 1) * share)
+        ref, spread = attend(q[0, rows], cache.k[0, at[:, 0], h, at[:, 1]], cache.v[0, at[:, 0], h, at[:, 1]],
+                             (~off).expand(share, n))
+        over = (o[0, rows].double() - ref).abs() - attention_bound(ref, spread)
+        assert float(over.max()) <= 0, (h, float(over.max()))
