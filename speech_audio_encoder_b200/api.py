@@ -658,6 +658,22 @@ def _list_operand(name: str, t: torch.Tensor | None, n: int | None = None) -> in
     return _operand(name, t, torch.int32, None if n is None else (n,))
 
 
+def _made(make, stream, returned: bool):
+    """make(): a tensor that the caller of a call on `stream` did not bring, allocated and filled on that stream, so
+    that the call's kernels come behind its fill and whatever gets its memory next comes behind them. One that is
+    returned is used on the current stream too: its memory then waits for both."""
+    if stream is None:
+        return make()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) > 1 else torch.cuda.default_stream()
+    current = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = make()
+    if returned and t.is_cuda:
+        t.record_stream(current)
+    return t
+
+
 def sal_attention_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, left: int = -1, right: int = -1,
                          sinks: int = 0, lengths: torch.Tensor | None = None, out: torch.Tensor | None = None,
                          stream=None) -> torch.Tensor:
@@ -668,7 +684,8 @@ def sal_attention_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, left
     B, H, T, hd = q.shape
     kvh = k.shape[1] if k.dim() == 4 else 0
     if out is None:
-        out = (torch.empty if lengths is None else torch.zeros)((B * T, H * hd), dtype=torch.bfloat16, device=q.device)
+        out = _made(lambda: (torch.empty if lengths is None else torch.zeros)((B * T, H * hd), dtype=torch.bfloat16,
+                                                                              device=q.device), stream, True)
     kv = (B, kvh, T, hd)
     _check("sal_attention_window", lib().sal_attention_window(
         _operand("q", q, torch.bfloat16), _operand("k", k, torch.bfloat16, kv), _operand("v", v, torch.bfloat16, kv), B,
@@ -682,7 +699,7 @@ def sal_attention_window_withhold(q: torch.Tensor, k: torch.Tensor, v: torch.Ten
     """Test hook: sal_attention_window with no key tile from ``tile`` on ever loaded, so a bounded wait gives up (read
     the outcome with sal_last_device_status)."""
     B, H, T, hd = q.shape
-    o = torch.empty((B * T, H * hd), dtype=torch.bfloat16, device=q.device)
+    o = _made(lambda: torch.empty((B * T, H * hd), dtype=torch.bfloat16, device=q.device), stream, True)
     _check("sal_attention_window_withhold", lib().sal_attention_window_withhold(
         _operand("q", q, torch.bfloat16), _operand("k", k, torch.bfloat16, q.shape),
         _operand("v", v, torch.bfloat16, q.shape), B, T, H, hd, _window(left, right, sinks), tile, o.data_ptr(), _stream(stream)))
@@ -799,7 +816,7 @@ def sal_cache_compact(cache: PagedCache, out: PagedCache | None = None, stream=N
 
 
 def attention_paged_workspace(cache: PagedCache, batch: int, heads: int) -> torch.Tensor:
-    """Scratch of sal_attention_paged (zero-filled, as its first use needs it)."""
+    """Scratch of sal_attention_paged (zero-filled on the current stream, as its first use needs it)."""
     n = lib().sal_attention_paged_workspace_bytes(cache.ref, batch, heads)
     return torch.zeros(max(n, 256), dtype=torch.uint8, device=cache.k.device)
 
@@ -816,9 +833,9 @@ def sal_attention_paged(q: torch.Tensor, cache: PagedCache, left: int = -1, sink
     if q.dtype is not torch.bfloat16 or q.get_device() != _current_device():
         raise ValueError("q: expected bfloat16 on the current CUDA device")
     if out is None:
-        out = torch.empty((B, H * hd), dtype=torch.bfloat16, device=q.device)
+        out = _made(lambda: torch.empty((B, H * hd), dtype=torch.bfloat16, device=q.device), stream, True)
     if workspace is None:
-        workspace = attention_paged_workspace(cache, B, H)
+        workspace = _made(lambda: attention_paged_workspace(cache, B, H), stream, False)
     _check("sal_attention_paged", lib().sal_attention_paged(
         q.data_ptr(), rows, heads, B, H, cache.ref, layer, 0 if seqs is None else _list_operand("seqs", seqs, B),
         _window(left, 0, sinks), _operand("out", out, torch.bfloat16, (B, H * hd)),
@@ -827,6 +844,7 @@ def sal_attention_paged(q: torch.Tensor, cache: PagedCache, left: int = -1, sink
 
 
 def stream_workspace(batch: int, T: int = 1, device="cuda") -> torch.Tensor:
+    """Scratch of sal_stream_prefill over T positions (1: of sal_stream_step)."""
     n = lib().sal_stream_workspace_bytes(batch, T)
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
@@ -840,9 +858,9 @@ def sal_stream_prefill(x: torch.Tensor, weights, n_layers: int, cache: PagedCach
     rec = weights.record if isinstance(weights, DeviceWeights) else weights
     B, T, width = x.shape
     if emb is None:
-        emb = torch.empty((B, T, width), dtype=torch.bfloat16, device=x.device)
+        emb = _made(lambda: torch.empty((B, T, width), dtype=torch.bfloat16, device=x.device), stream, True)
     if workspace is None:
-        workspace = stream_workspace(B, T, x.device)
+        workspace = _made(lambda: stream_workspace(B, T, x.device), stream, False)
     _check("sal_stream_prefill", lib().sal_stream_prefill(
         _operand("x", x, torch.float32, (B, T, WIDTH)), B, T, _list_operand("lengths", lengths, B), ctypes.byref(rec),
         n_layers, _window(left, 0, sinks), cache.ref, _list_operand("seqs", seqs, B),
@@ -859,9 +877,9 @@ def sal_stream_step(x: torch.Tensor, weights, n_layers: int, cache: PagedCache, 
     rec = weights.record if isinstance(weights, DeviceWeights) else weights
     B, width = x.shape
     if emb is None:
-        emb = torch.empty((B, width), dtype=torch.bfloat16, device=x.device)
+        emb = _made(lambda: torch.empty((B, width), dtype=torch.bfloat16, device=x.device), stream, True)
     if workspace is None:
-        workspace = stream_workspace(B, 1, x.device)
+        workspace = _made(lambda: stream_workspace(B, 1, x.device), stream, False)
     _check("sal_stream_step", lib().sal_stream_step(
         _operand("x", x, torch.float32, (B, WIDTH)), B, ctypes.byref(rec), n_layers, _window(left, 0, sinks), cache.ref,
         _list_operand("seqs", seqs, B), _operand("emb", emb, torch.bfloat16, x.shape),
