@@ -607,6 +607,10 @@ sal_status sal_attention_paged(const void* q, int64_t q_row_stride, int64_t q_he
  * before; emb [batch, 1280] bf16. A sequence may be named once. A row whose sequence is out of
  * range or empty, or whose page has been let go, keeps no key and value; its emb is that of a
  * position that sees what the cache has left of its keys.
+ * While the cache's status word is not zero neither call keeps any key or value, and emb means
+ * nothing: a resize that failed has left the old lengths, and the newest positions would be written
+ * over. After clearing the word resize the sequences back to the lengths that they had when it was
+ * last known to be zero (what has been granted since holds nothing) and go on from there.
  * Both clobber x. workspace: 256-byte aligned, sal_stream_workspace_bytes(batch, T) bytes (T = 1
  * for a step). Errors: as sal_encoder_forward, and as the cache calls. */
 size_t sal_stream_workspace_bytes(int batch, int64_t T);

@@ -854,7 +854,7 @@ def sal_stream_prefill(x: torch.Tensor, weights, n_layers: int, cache: PagedCach
                        emb: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                        stream=None) -> torch.Tensor:
     """x [batch, T, 1280] float32 (clobbered): the first positions of live streams -> emb [batch, T, 1280] bf16, their
-    keys and values kept in the cache (resize the sequences first)."""
+    keys and values kept in the cache (resize the sequences first; nothing is kept while ``cache.status`` is set)."""
     rec = weights.record if isinstance(weights, DeviceWeights) else weights
     B, T, width = x.shape
     if emb is None:
@@ -873,7 +873,8 @@ def sal_stream_step(x: torch.Tensor, weights, n_layers: int, cache: PagedCache, 
                     seqs: torch.Tensor | None = None, emb: torch.Tensor | None = None,
                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """x [batch, 1280] float32 (clobbered): one new position of each live stream -> emb [batch, 1280] bf16 (make the
-    sequences longer by one first, with sal_cache_resize)."""
+    sequences longer by one first, with sal_cache_resize; nothing is kept while ``cache.status`` is set, as a resize
+    that failed does)."""
     rec = weights.record if isinstance(weights, DeviceWeights) else weights
     B, width = x.shape
     if emb is None:

@@ -415,6 +415,7 @@ struct AppendArgs {
   const uint4 *k, *v;  // [batch, kv_heads, T] rows of row_vecs vectors
   uint4 *k_pages, *v_pages;
   const int32_t *table, *lengths, *starts, *seqs;
+  const uint32_t* failed;  // nothing is written where this is set (may be null)
   int T, kv_heads, row_shift;  // row_vecs = 1 << row_shift
   int sequences, max_pages, pages, page_shift;
 };
@@ -422,6 +423,7 @@ struct AppendArgs {
 __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
   pdl_wait();
   pdl_trigger();
+  if (a.failed && *SAL_CK_LD(a.failed, 4)) return;
   const int b = blockIdx.y;
   const int seq = a.seqs ? *SAL_CK_LD(a.seqs + b, 4) : b;
   if (seq < 0 || seq >= a.sequences) return;
@@ -558,16 +560,8 @@ using namespace sal;
     if (st_ != SAL_OK) return st_; \
   } while (0)
 
-extern "C" {
-
-size_t sal_cache_workspace_bytes(int pages, int sequences) {
-  if (pages <= 0 || sequences <= 0) return 0;
-  return ws_layout(pages, sequences).bytes;
-}
-
-sal_status sal_cache_append(const sal_cache* cache, int layer, const void* k, const void* v, int batch, int64_t T,
-                            const int32_t* starts, const int32_t* seqs, void* stream) {
-  const NvtxRange nvtx_("sal_cache_append");
+sal_status sal::cache_append(const sal_cache* cache, int layer, const void* k, const void* v, int batch, int64_t T,
+                             const int32_t* starts, const int32_t* seqs, bool unless_failed, cudaStream_t s) {
   SAL_TRY(check_cache(cache, false));
   if (batch < 0 || T < 0 || layer < 0 || layer >= cache->layers) return SAL_EINVAL;
   const int row_shift = cache->head_dim == 128 ? 4 : 3;
@@ -587,6 +581,7 @@ sal_status sal_cache_append(const sal_cache* cache, int layer, const void* k, co
   a.lengths = cache->lengths;
   a.starts = starts;
   a.seqs = seqs;
+  a.failed = unless_failed ? cache->status : nullptr;
   a.T = static_cast<int>(T);
   a.kv_heads = cache->kv_heads;
   a.row_shift = row_shift;
@@ -603,10 +598,24 @@ sal_status sal_cache_append(const sal_cache* cache, int layer, const void* k, co
   ck_declare(a.lengths, static_cast<uint64_t>(a.sequences) * 4, false);
   ck_declare(starts, static_cast<uint64_t>(batch) * 4, false);
   ck_declare(seqs, static_cast<uint64_t>(batch) * 4, false);
+  ck_declare(a.failed, 4, false);
   const dim3 grid(static_cast<unsigned>((row_vecs + 255) / 256), static_cast<unsigned>(batch));
-  return launch_kernel(append_kernel, grid, dim3(256), 0, static_cast<cudaStream_t>(stream), a) == cudaSuccess
+  return launch_kernel(append_kernel, grid, dim3(256), 0, s, a) == cudaSuccess
              ? SAL_OK
              : SAL_ECUDA;
+}
+
+extern "C" {
+
+size_t sal_cache_workspace_bytes(int pages, int sequences) {
+  if (pages <= 0 || sequences <= 0) return 0;
+  return ws_layout(pages, sequences).bytes;
+}
+
+sal_status sal_cache_append(const sal_cache* cache, int layer, const void* k, const void* v, int batch, int64_t T,
+                            const int32_t* starts, const int32_t* seqs, void* stream) {
+  const NvtxRange nvtx_("sal_cache_append");
+  return cache_append(cache, layer, k, v, batch, T, starts, seqs, false, static_cast<cudaStream_t>(stream));
 }
 
 sal_status sal_cache_copy_pages(const sal_cache* cache, const int32_t* src, const int32_t* dst, int n, void* stream) {

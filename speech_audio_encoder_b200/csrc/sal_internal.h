@@ -119,6 +119,9 @@ size_t attention_paged_zero_bytes();
 
 // cache.cu
 sal_status check_cache(const sal_cache* c, bool workspace);  // the members of a cache record
+// sal_cache_append; unless_failed: writes nothing while the cache's status word is set
+sal_status cache_append(const sal_cache* cache, int layer, const void* k, const void* v, int batch, int64_t T,
+                        const int32_t* starts, const int32_t* seqs, bool unless_failed, cudaStream_t s);
 
 // tensor maps (sal_api.cu)
 bool make_tmap_2d_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,

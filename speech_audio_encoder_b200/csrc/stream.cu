@@ -8,6 +8,10 @@
 // rotate-half pairs l, l + 64 and l + 32, l + 96) and puts k and v straight into their pages. Its
 // rotations come from a table that is built once a step, in 64 bits, since a stream's position
 // times the fastest frequency needs more than the 24 bits of fp32.
+//
+// Both write at the lengths that the resize before them left on the device. One that failed has
+// left the old lengths, and the newest position, whose page a fork may share, would be written
+// over: so while the cache's status word is set neither keeps anything.
 #define SAL_CK_FILE 9
 #include <cuda_bf16.h>
 #include <math.h>
@@ -61,6 +65,7 @@ struct StepArgs {
   float* rope;  // [2][batch][64]
   __nv_bfloat16 *q, *k_pages, *v_pages;
   const int32_t *table, *lengths, *seqs;
+  const uint32_t* failed;  // the cache's status word
   int batch, pages, page_shift, sequences, max_pages;
 };
 
@@ -124,7 +129,7 @@ __global__ void __launch_bounds__(256) step_qkv_kernel(const StepArgs a) {
     *SAL_CK_ST(a.q + static_cast<int64_t>(unit) * kHeadDim + lane + 32 * e, 2) = __float2bfloat16(x[e]);
   int seq;
   const int p = position_of(a, b, seq);
-  if (p < 0) return;
+  if (p < 0 || *SAL_CK_LD(a.failed, 4)) return;
   const int page = *SAL_CK_LD(a.table + static_cast<int64_t>(seq) * a.max_pages + (p >> a.page_shift), 4);
   if (page < 0 || page >= a.pages) return;
   const int64_t at = (((static_cast<int64_t>(page) * kHeads + h) << a.page_shift) + (p & ((1 << a.page_shift) - 1))) *
@@ -194,7 +199,7 @@ sal_status sal_stream_prefill(float* x, int batch, int64_t T, const int32_t* len
     SAL_TRY(layernorm_launch(x, M, L.ln1_g, L.ln1_b, ws.h, s));
     QkvOut qo{ws.q, ws.k, ws.v, L.qn_g, L.kn_g, ws.rope, T, 0};
     SAL_TRY(gemm_launch(kEpiQkv, ws.h, M, kWidth, L.w_qkv, 3 * kWidth, L.b_qkv, nullptr, &qo, s));
-    SAL_TRY(sal_cache_append(cache, i, ws.k, ws.v, batch, T, nullptr, seqs, stream));
+    SAL_TRY(cache_append(cache, i, ws.k, ws.v, batch, T, nullptr, seqs, true, s));
     SAL_TRY(window_attention_launch(ws.q, ws.k, ws.v, batch, T, kHeads, kHeads, kHeadDim, win, lengths, ws.o, s));
     SAL_TRY(gemm_launch(SAL_EPI_RESID_F32, ws.o, M, kWidth, L.w_o, kWidth, L.b_o, x, nullptr, s));
     SAL_TRY(layernorm_launch(x, M, L.ln2_g, L.ln2_b, ws.h, s));
@@ -222,6 +227,7 @@ sal_status sal_stream_step(float* x, int batch, const sal_weights* w, int n_laye
   a.table = cache->table;
   a.lengths = cache->lengths;
   a.seqs = seqs;
+  a.failed = cache->status;
   a.batch = batch;
   a.pages = cache->pages;
   a.page_shift = __builtin_ctz(static_cast<unsigned>(cache->page_size));
@@ -253,6 +259,7 @@ sal_status sal_stream_step(float* x, int batch, const sal_weights* w, int n_laye
     ck_declare(a.qkv, static_cast<uint64_t>(batch) * 3 * kWidth * 4, false);
     ck_declare(a.qn_g, kHeadDim * 2, false);
     ck_declare(a.kn_g, kHeadDim * 2, false);
+    ck_declare(a.failed, 4, false);
     ck_declare(a.q, static_cast<uint64_t>(batch) * kWidth * 2, true);
     ck_declare(a.k_pages, static_cast<uint64_t>(slab) * 2, true);
     ck_declare(a.v_pages, static_cast<uint64_t>(slab) * 2, true);
