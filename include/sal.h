@@ -497,6 +497,7 @@ sal_status sal_attention_window_withhold(const void* q, const void* k, const voi
 /* Bits of a cache's status word (device memory; the calls set bits and never clear them). */
 #define SAL_CACHE_NO_PAGES 1u /* a sequence could not grow: too few free pages */
 #define SAL_CACHE_BAD_LIST 2u /* an index or length out of range, or a sequence named twice */
+#define SAL_CACHE_LOST 4u     /* a sequence could not grow: its partly filled last page has been let go */
 
 /* A paged key/value cache: a record of the caller's device buffers (the record itself is
  * host memory, read during a call only). Position p of sequence s is row p % page_size of
@@ -564,10 +565,12 @@ sal_status sal_cache_fork(const sal_cache* cache, const int32_t* src, const int3
  * no position from min(old, new length) on can see. First all listed sequences are cut and
  * their unseen pages let go; then, in the order of the list, each that grows gets a page
  * for every new table entry, and a replacement for a partly filled last page that is
- * shared with another row (its contents copied in every layer) or that was let go. The
- * pages handed out are the free ones in ascending order. Entries past a listed sequence's
- * last page become -1. Too few free pages set SAL_CACHE_NO_PAGES, and the call changes
- * nothing. */
+ * shared with another row (its contents copied in every layer). The pages handed out are the
+ * free ones in ascending order. Entries past a listed sequence's last page become -1.
+ * A sequence that was cut back to the inside of a page which has been let go cannot grow from
+ * there (the lost positions of the page would become visible with whatever a new page holds): cut
+ * it to a multiple of page_size first. Such a growth sets SAL_CACHE_LOST, too few free pages
+ * set SAL_CACHE_NO_PAGES, and then the call changes nothing. */
 sal_status sal_cache_resize(const sal_cache* cache, const int32_t* seqs, const int32_t* new_lengths, int n,
                             const sal_window* window, int32_t* table_out, int32_t* lengths_out, void* stream);
 

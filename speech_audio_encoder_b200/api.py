@@ -77,7 +77,7 @@ class sal_cache(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t)]
 
 
-CACHE_NO_PAGES, CACHE_BAD_LIST = 1, 2  # bits of a cache's status word (sal.h)
+CACHE_NO_PAGES, CACHE_BAD_LIST, CACHE_LOST = 1, 2, 4  # bits of a cache's status word (sal.h)
 
 
 KIND_NAMES = ["rope_table", "layernorm", "qkv", "attention", "out_proj", "ffn_up", "ffn_down"]
@@ -712,7 +712,7 @@ class PagedCache:
     k, v [layers, pages, kv_heads, page_size, head_dim] bf16, table [sequences, max_pages] int32 and lengths
     [sequences] int32 (the tables are the whole state: a page that no row uses is free). ``empty`` makes a cache
     without sequences; ``with_tables`` makes another view of the same pages, for calls that leave the old tables valid.
-    Failed operations set bits of ``status`` (CACHE_NO_PAGES, CACHE_BAD_LIST); ``check`` reads it.
+    Failed operations set bits of ``status`` (CACHE_NO_PAGES, CACHE_BAD_LIST, CACHE_LOST); ``check`` reads it.
     """
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor,
@@ -756,7 +756,8 @@ class PagedCache:
         if bits:
             self.status.zero_()
             what = [w for b, w in ((CACHE_NO_PAGES, "too few free pages"),
-                                   (CACHE_BAD_LIST, "a list with an index or length out of range, or a sequence twice"))
+                                   (CACHE_BAD_LIST, "a list with an index or length out of range, or a sequence twice"),
+                                   (CACHE_LOST, "growth from inside a page that has been let go"))
                     if bits & b]
             raise RuntimeError("cache operation failed: " + "; ".join(what))
 

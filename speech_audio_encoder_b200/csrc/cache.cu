@@ -132,14 +132,20 @@ __device__ __forceinline__ int kept_page(const PlanArgs& a, const Entry& e, int 
   return p >= 0 && p < a.t.pages ? p : -1;
 }
 
-// Whether the entry's partly filled last page has to be replaced before it grows, and by
-// a copy of which page (-1: an empty one).
+// Whether the entry grows from inside a page that has been let go. The page's lost positions are
+// invisible because its entry names no page: with a page for the new ones they would be visible again
+// and hold whatever it held last.
+__device__ __forceinline__ bool grows_from_lost(const PlanArgs& a, const Entry& e) {
+  return e.len > e.kept && (e.kept & ((1 << a.t.page_shift) - 1)) && kept_page(a, e, e.kept >> a.t.page_shift) < 0;
+}
+
+// Whether the entry's partly filled last page (it is there) is shared, so that it has to be replaced by
+// a copy of itself, page `from`, before it grows.
 __device__ __forceinline__ bool replaces(const PlanArgs& a, const Entry& e, const uint32_t* multi, int& from) {
   from = -1;
   if (e.len <= e.kept || !(e.kept & ((1 << a.t.page_shift) - 1))) return false;
   const int p = kept_page(a, e, e.kept >> a.t.page_shift);
-  if (p < 0) return true;
-  if (!((multi[p >> 5] >> (p & 31)) & 1u)) return false;
+  if (p < 0 || !((multi[p >> 5] >> (p & 31)) & 1u)) return false;
   from = p;
   return true;
 }
@@ -152,12 +158,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1) resize_kernel(const PlanArgs 
   uint32_t* multi = sm + words;     // ... that more than one names
   uint32_t* listed = multi + words;  // sequences on the list
   __shared__ int warp_sums[33];
-  __shared__ int bad, n_pairs;
+  __shared__ int bad, lost, n_pairs;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
   for (int i = tid; i < 2 * words + seq_words; i += kPlanThreads) sm[i] = 0;
-  if (tid == 0) bad = n_pairs = 0;
+  if (tid == 0) bad = lost = n_pairs = 0;
   __syncthreads();
   const int capacity = t.max_pages << t.page_shift;
   for (int i = tid; i < a.n; i += kPlanThreads) {
@@ -205,6 +211,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) resize_kernel(const PlanArgs 
     int need = 0, from;
     if (i < a.n) {
       const Entry e = entry_of(a, i);
+      if (grows_from_lost(a, e)) lost = 1;
       need = min(pages_of(e.len, t.page_shift) - pages_of(e.kept, t.page_shift) + replaces(a, e, multi, from),
                  t.pages + 1);
     }
@@ -222,10 +229,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) resize_kernel(const PlanArgs 
   int mine = 0, n_free;
   for (int w = w0; w < w1; ++w) mine += __popc(free_bits(w));
   int rank = block_scan(mine, warp_sums, n_free);
-  if (asked > n_free) {
+  if (lost || asked > n_free) {
     for (int i = warp; i < a.n; i += kPlanThreads / 32) pass_row(t, *SAL_CK_LD(a.seqs + i, 4));
     if (tid == 0) {
-      atomicOr(SAL_CK_ST(t.status, 4), SAL_CACHE_NO_PAGES);
+      atomicOr(SAL_CK_ST(t.status, 4), lost ? SAL_CACHE_LOST : SAL_CACHE_NO_PAGES);
       *SAL_CK_ST(a.count, 4) = 0;
     }
     return;
@@ -255,7 +262,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) resize_kernel(const PlanArgs 
     }
     if (lane == 0) {
       *SAL_CK_ST(t.lengths_out + e.seq, 4) = e.len;
-      if (from >= 0) *SAL_CK_ST(a.pairs + atomicAdd(&n_pairs, 1), 8) = make_int2(from, *SAL_CK_LD(mine_free, 4));
+      if (swap) *SAL_CK_ST(a.pairs + atomicAdd(&n_pairs, 1), 8) = make_int2(from, *SAL_CK_LD(mine_free, 4));
     }
   }
   __syncthreads();
