@@ -534,7 +534,9 @@ size_t sal_cache_workspace_bytes(int pages, int sequences);
  * seqs[b] (NULL: b). Tokens at positions outside [0, lengths[seq]), or whose page has been
  * let go, and rows with a sequence out of range, are skipped: so a row may bring fewer than
  * T tokens, and one whose sal_cache_resize failed writes nothing. Two tokens for one
- * position (a sequence named twice, or a page that two rows share) leave one of them there. */
+ * position (a sequence named twice, or a page that two rows share) leave unspecified contents
+ * there, which may be parts of both. Errors: SAL_EINVAL, SAL_ESHAPE (batch > 65,535, T > 2^28, or
+ * kv_heads * T * head_dim > 2^34), SAL_EDEVICE, SAL_ECUDA. */
 sal_status sal_cache_append(const sal_cache* cache, int layer, const void* k, const void* v, int batch, int64_t T,
                             const int32_t* starts, const int32_t* seqs, void* stream);
 

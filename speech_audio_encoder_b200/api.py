@@ -771,7 +771,8 @@ class PagedCache:
 
 def sal_cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor | None,
                      seqs: torch.Tensor | None = None, layer: int = 0, stream=None) -> None:
-    """k, v [batch, kv_heads, T, head_dim] bf16 into positions starts[b] + t (None: t) of sequences seqs[b] (None: b)."""
+    """k, v [batch, kv_heads, T, head_dim] bf16 into positions starts[b] + t (None: t) of sequences seqs[b] (None: b).
+    Two tokens for one position leave unspecified contents there."""
     B, kvh, T, hd = k.shape
     if kvh != cache.kv_heads or hd != cache.head_dim:
         raise ValueError(f"k: the cache has {cache.kv_heads} heads of {cache.head_dim}")
