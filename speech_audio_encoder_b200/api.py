@@ -623,8 +623,12 @@ def attention_plan(batch: int, T: int, heads: int = 10, head_dim: int = 128, sms
 
 # ----------------------------------------------------------------------------- live streams
 
-_current_device = torch._C._cuda_getDevice
 _windows: dict = {}
+
+
+def _current_device() -> int:
+    # (looked up at the call: a torch without CUDA has no such function, and host-side calls need none)
+    return torch._C._cuda_getDevice()
 
 
 def _window(left: int, right: int, sinks: int):

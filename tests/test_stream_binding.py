@@ -1,6 +1,9 @@
 """The binding of the live-stream calls on the CPU, with a library that only records what it is
 given: on which stream the tensors are made that a caller leaves out."""
 import contextlib
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -90,3 +93,15 @@ def test_what_a_call_makes_belongs_to_its_stream(fake, name):
         call()
         assert fake.made and all(on is stream for _, on in fake.made), fake.made
         assert fake.calls[-1][1][-1] == (0 if stream is None else stream.cuda_stream)
+
+
+def test_the_binding_imports_where_torch_has_no_cuda():
+    """Host-side calls work on a torch that was built without CUDA functions."""
+    code = ("import torch\n"
+            "for name in ('_cuda_getDevice', '_cuda_getCurrentRawStream'):\n"
+            "    delattr(torch._C, name)\n"
+            "from speech_audio_encoder_b200 import api, build\n"
+            "build.build(quiet=True)\n"
+            "assert api.sal_cache and api.position_count(16000) > 0\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], cwd=root, check=True)
