@@ -736,8 +736,15 @@ class PagedCache:
             page_size, head_dim, sequences, max_pages, _operand("table", table, torch.int32),
             _operand("lengths", lengths, torch.int32, (sequences,)), _operand("status", status, torch.int32, (1,)),
             _operand("workspace", workspace, torch.uint8), workspace.numel())
-        self.ref = ctypes.byref(self.record)
+        self.device, self._ref = k.get_device(), ctypes.byref(self.record)
         self.pool, self.places = k.data_ptr(), (self.record.table, self.record.lengths)
+
+    @property
+    def ref(self):
+        """The record by reference, for a call on the current device."""
+        if self.device != _current_device():
+            raise ValueError("cache: must be on the current CUDA device")
+        return self._ref
 
     @classmethod
     def empty(cls, layers: int, pages: int, kv_heads: int, page_size: int, head_dim: int, sequences: int,
@@ -823,7 +830,7 @@ def sal_cache_compact(cache: PagedCache, out: PagedCache | None = None, stream=N
 
 def attention_paged_workspace(cache: PagedCache, batch: int, heads: int) -> torch.Tensor:
     """Scratch of sal_attention_paged (zero-filled on the current stream, as its first use needs it)."""
-    n = lib().sal_attention_paged_workspace_bytes(cache.ref, batch, heads)
+    n = lib().sal_attention_paged_workspace_bytes(cache._ref, batch, heads)
     return torch.zeros(max(n, 256), dtype=torch.uint8, device=cache.k.device)
 
 

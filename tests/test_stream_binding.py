@@ -105,3 +105,34 @@ def test_the_binding_imports_where_torch_has_no_cuda():
             "assert api.sal_cache and api.position_count(16000) > 0\n")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     subprocess.run([sys.executable, "-c", code], cwd=root, check=True)
+
+
+def test_a_cache_on_another_device_is_refused(fake, monkeypatch):
+    """Its addresses mean nothing to the current device: no call is made with them."""
+    cache, q, x, rec = _cache(), _bf16(2, 10, 128), torch.ones(2, 1280), api.sal_weights()
+    kv = _bf16(1, 10, 1, 128)
+    on_two = torch.empty(1, dtype=torch.int8)  # stands for an operand on the current device, 2
+
+    class Other(torch.Tensor):
+        def get_device(self):
+            return 2
+
+    def there(t):
+        return t.as_subclass(Other)
+
+    monkeypatch.setattr(api, "_current_device", lambda: 2)
+    assert there(on_two).get_device() == 2
+    fake.calls.clear()
+    lists = there(_ints(1))
+    for call in (lambda: api.sal_cache_compact(cache), lambda: api.sal_cache_fork(cache, lists, lists),
+                 lambda: api.sal_cache_resize(cache, lists, lists), lambda: api.sal_cache_copy_pages(cache, lists, lists),
+                 lambda: api.sal_cache_append(cache, there(kv), there(kv), None),
+                 lambda: api.sal_attention_paged(there(q), cache, out=there(_bf16(2, 1280)),
+                                                 workspace=there(torch.ones(4096, dtype=torch.uint8))),
+                 lambda: api.sal_stream_prefill(there(x[:, None].contiguous()), rec, 0, cache, emb=there(_bf16(2, 1, 1280)),
+                                                workspace=there(torch.ones(4096, dtype=torch.uint8))),
+                 lambda: api.sal_stream_step(there(x), rec, 0, cache, emb=there(_bf16(2, 1280)),
+                                             workspace=there(torch.ones(4096, dtype=torch.uint8)))):
+        with pytest.raises(ValueError, match="device"):
+            call()
+    assert not fake.calls
