@@ -763,9 +763,11 @@ class PagedCache:
 
     def check(self) -> None:
         """Waits for the device and raises if an operation has failed since the last check."""
+        torch.cuda.synchronize(self.status.device)  # the operations may run on other streams than the current one
         bits = int(self.status.item())
         if bits:
             self.status.zero_()
+            torch.cuda.synchronize(self.status.device)
             what = [w for b, w in ((CACHE_NO_PAGES, "too few free pages"),
                                    (CACHE_BAD_LIST, "a list with an index or length out of range, or a sequence twice"),
                                    (CACHE_LOST, "growth from inside a page that has been let go"))

@@ -85,3 +85,18 @@ def test_prefill_and_step():
             torch.cuda.synchronize()
             assert float((got.double() - first).norm() / first.norm()) < 1e-2
     cache.check()
+
+
+def test_check_waits_for_the_cache_operations():
+    """An operation that fails on another stream, behind 10 ms of work there, is not missed."""
+    api = _api()
+    cache = api.PagedCache.empty(1, 4, 1, 8, 64, 2, 9)
+    seqs, new, side = _ints([0, 1]), _ints([72, 72]), torch.cuda.Stream(priority=0)
+    api.sal_cache_resize(cache, seqs, _ints([1, 1]))
+    cache.check()
+    with torch.cuda.stream(side):
+        _busy()
+    api.sal_cache_resize(cache, seqs, new, stream=side)
+    with pytest.raises(RuntimeError, match="too few free pages"):
+        cache.check()
+    cache.check()
