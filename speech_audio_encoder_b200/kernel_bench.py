@@ -5,7 +5,9 @@
 KIND is one of frontend, stack_proj, layernorm, qkv, attention, out_proj, ffn_up, ffn_down,
 speaker_fuse, connector, ctc (the whole CTC adapter), attention64 (its 16 heads of 64),
 window and paged (attention with --left, --right and --sinks over clips of T positions, and of
-one position over a paged cache of T; --heads, --kv-heads, --head-dim), linear (any --N, --K, --epi).
+one position over a paged cache of T; --heads, --kv-heads, --head-dim), resize, step and prefill (one
+position more for streams of T positions, the --layers over it, and the same layers over whole clips
+of T), linear (any --N, --K, --epi).
 Each repetition is one launch (qkv also launches the small RoPE-table kernel). The
 repetitions are captured once as a CUDA graph and the replay is timed with CUDA events on
 the launching stream after warm-up (eager launches from Python would measure the host). Prints one JSON line with the
@@ -44,7 +46,8 @@ def main():
     ap.add_argument("--left", type=int, default=-1, help="window, paged: visible positions before (-1: all)")
     ap.add_argument("--right", type=int, default=0, help="window: visible positions after (-1: all)")
     ap.add_argument("--sinks", type=int, default=0, help="window, paged: first positions that stay visible")
-    ap.add_argument("--page", type=int, default=16, help="paged: positions of a page")
+    ap.add_argument("--page", type=int, default=16, help="paged, resize, step, prefill: positions of a page")
+    ap.add_argument("--layers", type=int, default=32, help="step, prefill: layers of the encoder")
     a = ap.parse_args()
     B, T = a.batch, a.T
     M = B * T
@@ -108,6 +111,42 @@ def main():
 
         def run():
             api.sal_attention_paged(q, cache, a.left, a.sinks, out=out, workspace=ws)
+    elif a.kind in ("resize", "step", "prefill"):
+        # streams whose pages behind the window have been let go, as resize leaves them
+        layers = 1 if a.kind == "resize" else a.layers
+        per, low = -(-(T + 1) // a.page), max(0, T - a.left) if a.left >= 0 else 0
+        kept = [c for c in range(per) if a.kind == "prefill" or (c + 1) * a.page > low or c * a.page < a.sinks]
+        pages = B * (len(kept) + 2)
+        order = torch.from_numpy(np.random.default_rng(0).permutation(pages).astype(np.int32)).cuda()
+        table = torch.full((B, per), -1, dtype=torch.int32, device="cuda")
+        table[:, kept] = order[:B * len(kept)].reshape(B, len(kept))
+        lens = torch.full((B,), T, dtype=torch.int32, device="cuda")
+        pool = [torch.empty((layers, pages, 10, a.page, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        for x in pool:
+            for layer in x:
+                layer.normal_()
+        cache = api.PagedCache(*pool, table, lens)
+        if a.kind == "resize":
+            after, longer = cache.with_tables(table.clone(), lens.clone()), lens + 1
+            seqs = torch.arange(B, dtype=torch.int32, device="cuda")
+
+            def run():
+                api.sal_cache_resize(cache, seqs, longer, a.left, a.sinks, out=after)
+        else:
+            dw = api.DeviceWeights(synth.make_weights(layers))
+            rows, seen = (M, M) if a.kind == "prefill" else (B, B * (T - low + min(a.sinks, low)))
+            # each weight once (2 bytes), and for a step each visible key and value
+            bytes_ = layers * (2.0 * 1280 * (4 * 1280 + 2 * 5120) + (5120.0 * seen if a.kind == "step" else 0.0))
+            flops = 2.0 * rows * layers * 1280 * (4 * 1280 + 2 * 5120)
+            x = torch.randn((B, T, 1280) if a.kind == "prefill" else (B, 1280), device="cuda")
+            emb = torch.empty(x.shape, dtype=torch.bfloat16, device="cuda")
+            ws = api.stream_workspace(B, T if a.kind == "prefill" else 1)
+
+            def run():
+                if a.kind == "prefill":
+                    api.sal_stream_prefill(x, dw, layers, cache, a.left, a.sinks, emb=emb, workspace=ws)
+                else:
+                    api.sal_stream_step(x, dw, layers, cache, a.left, a.sinks, emb=emb, workspace=ws)
     elif a.kind == "speaker_fuse":
         H = _bf16((M, 1280), 7, 1.0)
         P = torch.from_numpy(synth.speaker_activity(M, 1)).cuda()
