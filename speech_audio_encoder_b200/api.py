@@ -626,9 +626,11 @@ def attention_plan(batch: int, T: int, heads: int = 10, head_dim: int = 128, sms
 _windows: dict = {}
 
 
-def _current_device() -> int:
-    # (looked up at the call: a torch without CUDA has no such function, and host-side calls need none)
-    return torch._C._cuda_getDevice()
+def _no_device() -> int:
+    raise RuntimeError("this torch was built without CUDA")
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", _no_device)  # (host-side calls need none)
 
 
 def _window(left: int, right: int, sinks: int):
