@@ -28,8 +28,8 @@
 //
 // Measured on one B200, inputs larger than L2: an hour (44,999 positions, 10 heads of 128, 750 back
 // and 8 first positions) 259-270 us, 0.65-0.67 PFLOP/s, 40 % of what a large library product reaches
-// here; 2 x up to 8,191 positions with 32 heads on 2, 1,023 back, 201 us (0.77 PFLOP/s); head dim
-// 64, 44,998 x 16, 250 on either side 229 us; 16 clips of up to a minute 36 us; 374 positions 7.8 us.
+// here; 2 x up to 8,191 positions with 32 heads on 2, 1,023 back, 198 us (0.78 PFLOP/s); head dim
+// 64, 44,998 x 16, 250 on either side 224 us; 16 clips of up to a minute 36 us; 374 positions 7.8 us.
 // What bounds it is the softmax's chain: S into registers, maximum, exponentials, P back, with two
 // warps per scheduler to hide its latencies; counters of the hour: tensor pipe 41 %, exp2 unit 44 %,
 // issue 43 %. A pair of tiles takes about 4,000 clocks, of which the products are 2,080.
@@ -263,8 +263,8 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
 // of keys that begins at row ki, with the maximum and the sum of weights that are known. 32 keys at a
 // time, a score to a lane; then every lane adds up its columns.
 template <int HD>
-__device__ __forceinline__ void sum_again(const WindowArgs& a, int64_t qi, int64_t ki, int lo, int mid, int hi, float m,
-                                          float inv_l, __nv_bfloat16* dst) {
+__device__ __forceinline__ void sum_row(const WindowArgs& a, int64_t qi, int64_t ki, int lo, int mid, int hi, float m,
+                                        float inv_l, __nv_bfloat16* dst) {
   constexpr int kCols = HD / 32;
   const int lane = threadIdx.x & 31, count = lo + max(0, hi - mid);
   float o[kCols] = {};
@@ -272,16 +272,16 @@ __device__ __forceinline__ void sum_again(const WindowArgs& a, int64_t qi, int64
   for (int t0 = 0; t0 < count; t0 += 32) {
     const int t = min(t0 + lane, count - 1), j = t < lo ? t : mid + t - lo, n = min(32, count - t0);
     float s = 0.f;
-#pragma unroll 4
-    for (int d = 0; d < HD; d += 8) {
+#pragma unroll 8
+    for (int d = 0; d < HD / 8; ++d) {
       float x[8], y[8];
-      unpack8(*SAL_CK_LD(reinterpret_cast<const uint4*>(a.q + qi * HD + d), 16), x);
-      unpack8(*SAL_CK_LD(reinterpret_cast<const uint4*>(a.k + (ki + j) * HD + d), 16), y);
+      unpack8(*SAL_CK_LD(reinterpret_cast<const uint4*>(a.q + qi * HD) + d, 16), x);
+      unpack8(*SAL_CK_LD(reinterpret_cast<const uint4*>(a.k + (ki + j) * HD) + d, 16), y);
 #pragma unroll
       for (int i = 0; i < 8; ++i) s = fmaf(x[i], y[i], s);
     }
     const float w = fast_exp2(fmaf(s, a.scale_log2, -m));
-#pragma unroll 4
+#pragma unroll 32
     for (int i = 0; i < n; ++i) {
       const float wi = __shfl_sync(0xffffffffu, w, i);
       const int ji = __shfl_sync(0xffffffffu, j, i);
@@ -301,6 +301,61 @@ __device__ __forceinline__ void sum_again(const WindowArgs& a, int64_t qi, int64
 #pragma unroll
   for (int e = 0; e < kCols; e += 2)
     *SAL_CK_ST(reinterpret_cast<uint32_t*>(dst + lane * kCols + e), 4) = pack_bf16x2(o[e] * inv_l, o[e + 1] * inv_l);
+}
+
+// Whether the lane's row, which sees the keys [lo, hi) and [0, sinks) below hi, does not see one of the
+// keys [from, to) that holds a value that is no number. A warp; 32 keys at a time, one to a lane.
+template <int HD>
+__device__ __forceinline__ bool hides_no_number(const WindowArgs& a, int64_t ki, int from, int to, int sinks, int lo,
+                                                int hi) {
+  const int lane = threadIdx.x & 31;
+  bool hidden = false;
+#pragma unroll 1
+  for (int j0 = from; j0 < to; j0 += 32) {
+    uint32_t bad = 0;
+    if (j0 + lane < to) {
+#pragma unroll 4
+      for (int d = 0; d < HD; d += 8) {
+        const uint4 u = *SAL_CK_LD(reinterpret_cast<const uint4*>(a.v + (ki + j0 + lane) * HD + d), 16);
+        for (const uint32_t w : {u.x, u.y, u.z, u.w})
+          bad |= (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+      }
+    }
+    const uint32_t seen = bits_between(lo - j0, hi - j0) | bits_between(0, min(sinks, hi) - j0);
+    hidden |= (__ballot_sync(0xffffffffu, bad != 0) & ~seen) != 0;
+  }
+  return hidden;
+}
+
+// The rows in `again` (a lane's row is p) of a warp's 32 that hide a value that is no number among the
+// keys of their tiles - those of the window [from, to), and `first` tiles of first positions - summed again.
+// An hour, 750 back: one NaN in every head 1.9 to 2.2 ms, only infinities 33 ms (clean 0.25); 8,192
+// positions that all see each other and a NaN 0.37 ms, as without (110 if each such row is summed again).
+// A function of its own: the same lines inside the loop cost head dim 64 2 % (instruction fetch).
+template <int HD>
+__device__ __noinline__ void sum_again(const WindowArgs& a, uint32_t again, int b, int head, int kv, int n, int p, int lo,
+                                       int hi, int from, int to, int first, float m, float inv_l) {
+  const int64_t plane = static_cast<int64_t>(kv) * a.T, rows = (static_cast<int64_t>(b) * a.heads + head) * a.T;
+  // keys of the window's tiles in front of what all rows of the warp see, and behind it; and those behind
+  // the first positions in their tiles, whether a tile of the window has them too or not
+  to = min(n, to);
+  const int lo31 = min(to, __shfl_sync(0xffffffffu, lo, 31)), hi0 = __shfl_sync(0xffffffffu, hi, 0);
+  bool hidden = false;
+#pragma unroll 1
+  for (int part = 0; part < (first > 0 ? 3 : 2); ++part)
+    hidden |= hides_no_number<HD>(a, plane, part == 0 ? from : part == 1 ? max(max(from, lo31), hi0) : a.sinks,
+                                  part == 0 ? lo31 : part == 1 ? to : min(n, (a.sinks + 15) & ~15),
+                                  first > 0 ? 0 : a.sinks, part == 2 ? 0 : lo, part == 2 ? 0 : hi);
+  again &= __ballot_sync(0xffffffffu, hidden);
+#pragma unroll 1
+  for (; again; again &= again - 1) {
+    const int r = __ffs(again) - 1;
+    auto of = [&](auto x) { return __shfl_sync(0xffffffffu, x, r); };
+    const int at = of(p), row_lo = of(lo), row_hi = of(hi);
+    __syncwarp();  // the row's own stores are behind these
+    sum_row<HD>(a, rows + at, plane, min(a.sinks, min(row_lo, row_hi)), row_lo, row_hi, of(m), of(inv_l),
+                a.o + ((static_cast<int64_t>(b) * a.T + at) * a.heads + head) * HD);
+  }
 }
 
 // Where everything is in shared memory.
@@ -517,7 +572,7 @@ __device__ __forceinline__ void drain_products(uint64_t* bar, bool ok, const Wai
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
     window_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                  const __grid_constant__ CUtensorMap tmV, const WindowArgs args) {
+                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ WindowArgs args) {
   using L = Layout<HD>;
   constexpr int NK = L::kStagesK, NV = L::kStagesV;
   extern __shared__ unsigned char smem_raw[];
@@ -775,7 +830,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++n_s;
       }
       if (!ok) break;
-      const bool stored = p < it.n;
+      const int n = it.n;
+      const bool stored = p < n;
       const int head = it.head[slot], b = it.b, kv = it.kv;
       __nv_bfloat16* dst = args.o + ((static_cast<int64_t>(b) * args.T + p) * args.heads + head) * HD;
       __syncwarp();
@@ -814,20 +870,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float zero_lo, zero_hi;
       f2_unpack(f2_add(f2_add(zeros[0], zeros[1]), f2_add(zeros[2], zeros[3])), zero_lo, zero_hi);
-      // A value that is no number, at a key of these tiles that the row need not see, has met a weight
-      // of zero: such a row is summed again over what it does see.
-      uint32_t again = __ballot_sync(0xffffffffu, stored && !(zero_lo + zero_hi == 0.f));
-#pragma unroll 1
-      for (; again; again &= again - 1) {
-        const int r = __ffs(again) - 1;
-        auto of = [&](auto x) { return __shfl_sync(0xffffffffu, x, r); };
-        const int lo = of(key_lo), hi = of(key_hi);
-        const int64_t at = of(p);
-        __syncwarp();  // the row's own stores are behind these
-        sum_again<HD>(args, (static_cast<int64_t>(b) * args.heads + head) * args.T + at, static_cast<int64_t>(kv) * args.T,
-                      min(args.sinks, min(lo, hi)), lo, hi, of(m_ref == -INFINITY ? 0.f : m_ref), of(inv_l),
-                      args.o + ((static_cast<int64_t>(b) * args.T + at) * args.heads + head) * HD);
-      }
+      // A value that is no number, at a key of these tiles that the row does not see, has met a weight of
+      // zero: such a row is summed again over what it does see. (One that only sees such values, or whose
+      // weights are no numbers, is as it should be.)
+      const uint32_t again = __ballot_sync(0xffffffffu, stored && l == l && !(zero_lo + zero_hi == 0.f));
+      if (again)
+        sum_again<HD>(args, again, b, head, kv, n, p, key_lo, key_hi, start + kKeys * (begin - first),
+                      start + kKeys * (last - first + 1), first, m_ref == -INFINITY ? 0.f : m_ref, inv_l);
       // (O is overwritten by the next item's first product, which waits for this slot's next P)
     }
   }
