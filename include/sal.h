@@ -605,8 +605,9 @@ sal_status sal_attention_paged(const void* q, int64_t q_row_stride, int64_t q_he
  * x0 of positions 0 .. lengths[b] - 1 (lengths int32 [batch], NULL: all T; rows past a length are
  * computed from what they hold and mean nothing) and, after the call, the residual stream; emb
  * [batch, T, 1280] bf16 the final LayerNorm of it. The keys and values go to sequence seqs[b]
- * (NULL: b), which sal_cache_resize must have given the length lengths[b] before; what the
- * window has already let go is not kept.
+ * (NULL: b), which sal_cache_resize must have given the length lengths[b] before, from a length of
+ * 0 (pages that a sequence has from before may be shared with a fork); what the window has already
+ * let go is not kept.
  * sal_stream_step takes one new position of each row's stream: x [batch, 1280] float32 is x0 of
  * position p = lengths[seq] - 1 of the cache, which sal_cache_resize must have made longer by one
  * before; emb [batch, 1280] bf16. A sequence may be named once. A row whose sequence is out of

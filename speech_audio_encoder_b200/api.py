@@ -738,13 +738,13 @@ class PagedCache:
             page_size, head_dim, sequences, max_pages, _operand("table", table, torch.int32),
             _operand("lengths", lengths, torch.int32, (sequences,)), _operand("status", status, torch.int32, (1,)),
             _operand("workspace", workspace, torch.uint8), workspace.numel())
-        self.device, self._ref = k.get_device(), ctypes.byref(self.record)
+        self.device_index, self._ref = k.get_device(), ctypes.byref(self.record)
         self.pool, self.places = k.data_ptr(), (self.record.table, self.record.lengths)
 
     @property
     def ref(self):
         """The record by reference, for a call on the current device."""
-        if self.device != _current_device():
+        if self.device_index != _current_device():
             raise ValueError("cache: must be on the current CUDA device")
         return self._ref
 

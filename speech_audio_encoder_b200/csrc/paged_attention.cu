@@ -18,7 +18,7 @@
 //   * many: all rows' keys in one line cut into equal parts; the pieces of a row are joined by the
 //     block that brings the last of them, or by a second small kernel.
 // Measured on one B200 with inputs larger than L2: 64 rows of up to 8,190 keys (10 heads of 128)
-// 261-268 us, 6.3 TB/s, 97 % of a plain copy's rate; 64 rows that see 758 of their 45,000 keys
+// 265-270 us, 6.2-6.3 TB/s, 95-97 % of a plain copy's rate; 64 rows that see 758 of their 45,000 keys
 // 50 us, of which 38 are bytes and the rest the start of a block's copies (page table, then keys) and
 // its end; 3 rows of up to 45,000 keys, 32 heads on 2, 30 us: 14 bytes, 3 to start, 3 to
 // merge the warps, 5 for the join. One row of 750 keys is 6 us on the device as clusters and 11 as

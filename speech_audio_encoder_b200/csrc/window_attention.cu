@@ -27,9 +27,9 @@
 // log2 units (a weight is then at most 256, which fp32 sums and bf16 hold as well as 1).
 //
 // Measured on one B200, inputs larger than L2: an hour (44,999 positions, 10 heads of 128, 750 back
-// and 8 first positions) 259-270 us, 0.65-0.67 PFLOP/s, 40 % of what a large library product reaches
-// here; 2 x up to 8,191 positions with 32 heads on 2, 1,023 back, 198 us (0.78 PFLOP/s); head dim
-// 64, 44,998 x 16, 250 on either side 224 us; 16 clips of up to a minute 36 us; 374 positions 7.8 us.
+// and 8 first positions) 259-271 us, 0.65-0.67 PFLOP/s, 40 % of what a large library product reaches
+// here; 2 x up to 8,191 positions with 32 heads on 2, 1,023 back, 197-202 us (0.77 PFLOP/s); head dim
+// 64, 44,998 x 16, 250 on either side 224-230 us; 16 clips of up to a minute 36 us; 374 positions 7.8 us.
 // What bounds it is the softmax's chain: S into registers, maximum, exponentials, P back, with two
 // warps per scheduler to hide its latencies; counters of the hour: tensor pipe 41 %, exp2 unit 44 %,
 // issue 43 %. A pair of tiles takes about 4,000 clocks, of which the products are 2,080.
